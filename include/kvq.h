@@ -117,6 +117,10 @@ typedef enum {
                                     of the sequences that CTA worked on come out
                                     as NaN and the call's output is not valid */
 
+#define KVQ_DEVERR_RANGE 0x10u    /* read, ragged attention: cu_tokens / cu_q not
+                                    rising from >= 0 to <= the token count */
+#define KVQ_DEVERR_POSITION 0x20u /* append_rope: position outside the angle table */
+
 typedef struct {
   int32_t num_blocks;         /* blocks in the pool */
   int32_t block_size;         /* tokens per block; must be 16 */
@@ -222,6 +226,80 @@ int kvq_pool_extend_seq(kvq_pool* pool, int32_t* block_table_row, int32_t cur_le
 int kvq_append(const void* k, const void* v, const int64_t* slot_mapping, int32_t num_tokens,
                void* k_cache, void* v_cache, void* k_scale, void* v_scale, kvq_fmt fmt,
                const kvq_dims* dims, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Quantize-on-append with the rotary embedding.                              */
+/* The form in which a decoder layer has its new tokens: q, k and v as views  */
+/* of one projection's output, not yet rotated. [COMPRESS] "5.1", "6.3": K and */
+/* V are quantized right after they are computed.                             */
+/* ------------------------------------------------------------------------ */
+typedef enum {
+  KVQ_ROPE_HALVES = 0,      /* pairs (i, i + rotary_dim / 2) */
+  KVQ_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1) */
+} kvq_rope_pairs;
+
+/*
+ * For each token t, with c_i = cos_sin[positions[t]][i] and
+ * s_i = cos_sin[positions[t]][rotary_dim / 2 + i], every pair (a, b) of the
+ * first rotary_dim channels of each q and k head becomes
+ *   a' = a c_i - b s_i,  b' = b c_i + a s_i
+ * (FP32, each product and sum rounded, then BF16; the other channels pass
+ * through). q_out receives the rotated query; the rotated k and v are
+ * quantized and stored exactly as kvq_append stores them.
+ *
+ * q             device, BF16: token t's n_q_heads * head_dim values begin at
+ *               q + t * q_stride elements. NULL together with q_out: no query.
+ * k, v          device, BF16: n_kv_heads * head_dim values per token, strides
+ *               k_stride, v_stride (each stride a multiple of 8, at least the
+ *               values of a token).
+ * positions     device, [num_tokens] int32. A token whose position is outside
+ *               [0, max_position) is skipped, its q_out row included, and sets
+ *               KVQ_DEVERR_POSITION unless its slot is negative.
+ * cos_sin       device, [max_position][rotary_dim] FP32: rotary_dim / 2
+ *               cosines, then the sines.
+ * rotary_dim    a multiple of 16, at most head_dim.
+ * q_out         device, [num_tokens][n_q_heads][head_dim] BF16, contiguous; not
+ *               overlapping q, k or v (KVQ_ERR_ARG). Written for skipped slots
+ *               (slot < 0) too.
+ * slot_mapping, the caches, scales and formats are those of kvq_append.
+ */
+int kvq_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, const int32_t* positions,
+                    const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                    kvq_rope_pairs pairs, const int64_t* slot_mapping, int32_t num_tokens,
+                    void* q_out, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                    kvq_fmt fmt, const kvq_dims* dims, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Dequantizing read-back.                                                    */
+/* [LIMITS] "What KV cache quantization actually is": what is read back is    */
+/* code * scale. For moving a prefix out of the pool, re-encoding it in       */
+/* another format, or handing it to a consumer that knows no pages; decode    */
+/* itself never needs it.                                                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * Row r of k_out / v_out, cu_tokens[b] <= r < cu_tokens[b+1], receives the
+ * dequantized K / V of token starts[b] + r - cu_tokens[b] of sequence b.
+ *
+ * cu_tokens     device, [n_seqs + 1] int32, non-decreasing within
+ *               [0, total_tokens] (else KVQ_DEVERR_RANGE, and which rows are
+ *               written is unspecified). Rows outside [cu_tokens[0],
+ *               cu_tokens[n_seqs]) are left as they were.
+ * starts        device, [n_seqs] int32: first token read of each sequence.
+ * block_tables  device, [n_seqs][max_blocks_per_seq] int32.
+ * k_out, v_out  device, [total_tokens][n_kv_heads][head_dim] BF16 or FP32; either
+ *               may be NULL. FP32 holds code * scale (INT8: (code - zp) * scale;
+ *               KIVI: code * s + z) with the one rounding of FP32; BF16 rounds
+ *               that to nearest even.
+ * fmt           any format. KIVI: k_cache, v_cache are the packed codes, scales
+ *               = {k_meta, v_meta}, and the runs lie in complete groups.
+ * A token past the block table (KVQ_DEVERR_CONTEXT) or on a block id outside
+ * the pool (KVQ_DEVERR_BLOCK) reads as zeros.
+ */
+int kvq_read(const void* k_cache, const void* v_cache, const void* const* scales,
+             const int32_t* block_tables, const int32_t* starts, const int32_t* cu_tokens,
+             int32_t n_seqs, int32_t total_tokens, void* k_out, void* v_out,
+             kvq_out_dtype out_dtype, kvq_fmt fmt, const kvq_dims* dims, kvq_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Paged GQA decode attention.                                                */
@@ -406,6 +484,51 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
                      void* out, kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
                      int32_t partition_tokens, kvq_fmt fmt, const kvq_dims* dims,
                      kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention of ragged chunks over the paged cache.                            */
+/* [GUIDE] "Core concepts 1)", "2)": one step of a server holds sequences that */
+/* prefill a chunk beside sequences that decode one token. This call takes     */
+/* them together, each sequence with its own number of new tokens.             */
+/* ------------------------------------------------------------------------ */
+/*
+ * Sequence b brings the new tokens cu_q[b] .. cu_q[b+1]-1 of the packed query:
+ * the last n_b = cu_q[b+1] - cu_q[b] tokens of its context, already appended.
+ * Row i of them stands at position p = context_lens[b] - n_b + i and attends
+ * the tokens t <= p, with a window > 0 those of p - window < t <= p:
+ *   out[cu_q[b] + i][h] = softmax_t(sm_scale * q[cu_q[b] + i][h] . K_b[t][h/G])
+ *                         weighted sum of V_b[t][h/G].
+ * A row that attends nothing (p < 0) is all zeros. Rows outside [cu_q[0],
+ * cu_q[n_seqs]) are left as they were.
+ *
+ * q        device, BF16: token r's n_q_heads * head_dim values begin at
+ *          q + r * q_stride elements (a multiple of 8, at least the values of
+ *          a token); a view of the fused projection's output will do.
+ * cu_q     device, [n_seqs + 1] int32, non-decreasing within [0, total_q]. A
+ *          sequence whose range is not so is skipped and sets KVQ_DEVERR_RANGE.
+ * out      device, [total_q][n_q_heads][head_dim], contiguous, BF16 or FP32 per
+ *          out_dtype; not overlapping q (KVQ_ERR_ARG). BF16: the softmax
+ *          weights enter the second product rounded to 11 bits (8 for a BF16
+ *          cache); FP32: to 22 (16) bits.
+ * window   0: none.
+ * workspace  at least kvq_ragged_attn_workspace_bytes(...) bytes, contents on
+ *          entry do not matter (0 from that call: invalid arguments).
+ * The other arguments are those of kvq_decode_attn. A context that is not legal
+ * (KVQ_DEVERR_CONTEXT) counts as empty: its rows are zeros. A token on a block
+ * id outside the pool (KVQ_DEVERR_BLOCK) is not attended. A token whose V row
+ * holds a NaN or an infinity (with a per-token scale: whose V scale is one)
+ * makes every channel of the rows that attend it NaN.
+ * No length is needed on the host: a captured graph may be replayed with other
+ * cu_q and context_lens of at most n_seqs sequences and total_q tokens.
+ */
+size_t kvq_ragged_attn_workspace_bytes(int32_t total_q, kvq_fmt fmt, const kvq_dims* dims);
+int kvq_ragged_attn(const void* q, int64_t q_stride, const int32_t* cu_q, int32_t n_seqs,
+                    int32_t total_q, const void* k_cache, const void* v_cache,
+                    const void* const* scales, const int32_t* block_tables,
+                    const int32_t* context_lens, int32_t max_context_len, int32_t window,
+                    float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace,
+                    size_t workspace_bytes, kvq_fmt fmt, const kvq_dims* dims,
+                    kvq_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* KIVI-style low-bit cache (KVQ_KIVI2, KVQ_KIVI4).                            */

@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,7 +25,8 @@ LIB = os.path.join(PKG, "libkvq.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["kvq_kernels.cu", "kvq_api.cpp", "kvq_pool.cpp", "kvq_noalloc.cu"]
+SOURCES = ["kvq_kernels.cu", "kvq_ragged.cu", "kvq_ops.cu", "kvq_api.cpp", "kvq_pool.cpp",
+           "kvq_noalloc.cu"]
 
 
 def nvcc() -> str:
@@ -54,15 +56,17 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(INCLUDE, "kvq.h")] + [
         os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    objs = []
-    log = []
-    for src in SOURCES:
+    objs = [os.path.join(BUILD, src + ".o") for src in SOURCES]
+
+    def compile_one(src, obj):
         path = os.path.join(CSRC, src)
-        obj = os.path.join(BUILD, src + ".o")
-        objs.append(obj)
-        if force or verbose_ptxas or _stale(obj, [path] + headers):
-            extra = ["-Xptxas", "-v"] if (verbose_ptxas and src.endswith(".cu")) else []
-            log.append(_run([nvcc()] + ARCH + COMMON + extra + ["-c", "-o", obj, path]))
+        if not (force or verbose_ptxas or _stale(obj, [path] + headers)):
+            return ""
+        extra = ["-Xptxas", "-v"] if (verbose_ptxas and src.endswith(".cu")) else []
+        return _run([nvcc()] + ARCH + COMMON + extra + ["-c", "-o", obj, path])
+
+    with ThreadPoolExecutor(len(SOURCES)) as ex:            # each compiler is its own process
+        log = list(ex.map(compile_one, SOURCES, objs))
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         _run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-ldl", "-lrt",

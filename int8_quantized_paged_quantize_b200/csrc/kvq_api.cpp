@@ -129,6 +129,123 @@ int kvq_append(const void* k, const void* v, const int64_t* slot_mapping, int32_
                                fmt, *dims, stream));
 }
 
+namespace {
+// Whether [a, a + an) and [b, b + bn) (bytes) share an address.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bn && y < x + an;
+}
+// A strided input: heads * D contiguous values per token, tokens `stride` apart.
+bool rows_ok(const void* p, int64_t stride, int32_t heads, int32_t D) {
+  return dev_ok(p) && stride >= int64_t(heads) * D && stride % 8 == 0;
+}
+size_t rows_bytes(int64_t stride, int32_t T, int32_t heads, int32_t D) {
+  return size_t(int64_t(T - 1) * stride + int64_t(heads) * D) * 2;
+}
+}  // namespace
+
+int kvq_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, const int32_t* positions,
+                    const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                    kvq_rope_pairs pairs, const int64_t* slot_mapping, int32_t num_tokens,
+                    void* q_out, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                    kvq_fmt fmt, const kvq_dims* dims, kvq_stream_t stream) {
+  if (!fmt_valid(fmt) || num_tokens < 0) return KVQ_ERR_ARG;
+  int rc = check_dims(dims);
+  if (rc != KVQ_OK) return rc;
+  const int32_t D = dims->head_dim, Hq = dims->n_q_heads, Hk = dims->n_kv_heads;
+  if (pairs != KVQ_ROPE_HALVES && pairs != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_ARG;
+  if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16 != 0 || max_position < 1)
+    return KVQ_ERR_ARG;
+  if (num_tokens == 0) return KVQ_OK;
+  if (!rows_ok(k, k_stride, Hk, D) || !rows_ok(v, v_stride, Hk, D) || !dev_ok(positions) ||
+      !dev_ok(cos_sin) || !dev_ok(slot_mapping) || !dev_ok(k_cache) || !dev_ok(v_cache))
+    return KVQ_ERR_ARG;
+  if (fmt != KVQ_BF16 && (!dev_ok(k_scale) || !dev_ok(v_scale))) return KVQ_ERR_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return KVQ_ERR_ARG;
+  if (q) {
+    if (!rows_ok(q, q_stride, Hq, D) || !dev_ok(q_out)) return KVQ_ERR_ARG;
+    const size_t out = size_t(num_tokens) * Hq * D * 2;
+    if (overlap(q_out, out, q, rows_bytes(q_stride, num_tokens, Hq, D)) ||
+        overlap(q_out, out, k, rows_bytes(k_stride, num_tokens, Hk, D)) ||
+        overlap(q_out, out, v, rows_bytes(v_stride, num_tokens, Hk, D)))
+      return KVQ_ERR_ARG;
+  }
+  const RopeArgs a{q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_position,
+                   rotary_dim, pairs == KVQ_ROPE_INTERLEAVED, q_out};
+  return cuda_rc(launch_append_rope(a, slot_mapping, num_tokens, k_cache, v_cache, k_scale, v_scale,
+                                    fmt, *dims, stream));
+}
+
+int kvq_read(const void* k_cache, const void* v_cache, const void* const* scales,
+             const int32_t* block_tables, const int32_t* starts, const int32_t* cu_tokens,
+             int32_t n_seqs, int32_t total_tokens, void* k_out, void* v_out,
+             kvq_out_dtype out_dtype, kvq_fmt fmt, const kvq_dims* dims, kvq_stream_t stream) {
+  if ((!fmt_valid(fmt) && !fmt_kivi(fmt)) || n_seqs < 0 || total_tokens < 0) return KVQ_ERR_ARG;
+  int rc = check_dims(dims);
+  if (rc != KVQ_OK) return rc;
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_ERR_ARG;
+  if (n_seqs == 0 || total_tokens == 0) return KVQ_OK;
+  if ((!k_out && !v_out) || (k_out && !dev_ok(k_out)) || (v_out && !dev_ok(v_out)))
+    return KVQ_ERR_ARG;
+  if (!dev_ok(k_cache) || !dev_ok(v_cache) || !dev_ok(block_tables) || !dev_ok(starts) ||
+      !dev_ok(cu_tokens))
+    return KVQ_ERR_ARG;
+  const void *ks = nullptr, *vs = nullptr;
+  if (fmt != KVQ_BF16) {
+    if (!scales || !dev_ok(scales[0]) || !dev_ok(scales[1])) return KVQ_ERR_ARG;
+    ks = scales[0];
+    vs = scales[1];
+  }
+  const size_t out = size_t(total_tokens) * dims->n_kv_heads * dims->head_dim *
+                     (out_dtype == KVQ_OUT_F32 ? 4 : 2);
+  if (overlap(k_out, out, v_out, out)) return KVQ_ERR_ARG;
+  const ReadArgs a{k_cache, v_cache, ks, vs, block_tables, starts, cu_tokens, n_seqs, total_tokens,
+                   k_out, v_out, out_dtype == KVQ_OUT_F32};
+  return cuda_rc(launch_read(a, fmt, *dims, stream));
+}
+
+size_t kvq_ragged_attn_workspace_bytes(int32_t total_q, kvq_fmt fmt, const kvq_dims* dims) {
+  if (!fmt_valid(fmt) || total_q < 1 || check_dims(dims) != KVQ_OK) return 0;
+  return ragged_workspace(total_q, *dims);
+}
+
+int kvq_ragged_attn(const void* q, int64_t q_stride, const int32_t* cu_q, int32_t n_seqs,
+                    int32_t total_q, const void* k_cache, const void* v_cache,
+                    const void* const* scales, const int32_t* block_tables,
+                    const int32_t* context_lens, int32_t max_context_len, int32_t window,
+                    float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace,
+                    size_t workspace_bytes, kvq_fmt fmt, const kvq_dims* dims,
+                    kvq_stream_t stream) {
+  if (n_seqs < 0 || total_q < 0 || window < 0) return KVQ_ERR_ARG;
+  DecodePlan plan;
+  int rc = check_decode_common(n_seqs, max_context_len, 0, fmt, dims, &plan);
+  if (rc != KVQ_OK) return rc;
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_ERR_ARG;
+  if (n_seqs == 0 || total_q == 0) return KVQ_OK;
+  const int32_t D = dims->head_dim, Hq = dims->n_q_heads;
+  // query rows of one KV head, and positions, are counted in 32 bits
+  if (int64_t(total_q) * (Hq / dims->n_kv_heads) > (int64_t(1) << 30) ||
+      max_context_len > (int32_t(1) << 30))
+    return KVQ_ERR_UNSUPPORTED;
+  const void *ks, *vs;
+  rc = check_decode_inputs(q, k_cache, v_cache, scales, block_tables, context_lens, sm_scale, fmt,
+                           &ks, &vs);
+  if (rc != KVQ_OK) return rc;
+  if (!rows_ok(q, q_stride, Hq, D) || !dev_ok(cu_q) || !dev_ok(out) || !dev_ok(workspace))
+    return KVQ_ERR_ARG;
+  if (workspace_bytes < ragged_workspace(total_q, *dims)) return KVQ_ERR_WORKSPACE;
+  // blocks are read and written by different CTAs at different times
+  if (overlap(out, size_t(total_q) * Hq * D * (out_dtype == KVQ_OUT_F32 ? 4 : 2), q,
+              rows_bytes(q_stride, total_q, Hq, D)))
+    return KVQ_ERR_ARG;
+  if (window >= max_context_len) window = 0;          // hides nothing
+  const RaggedArgs a{q, q_stride, cu_q, n_seqs, total_q, k_cache, v_cache, ks, vs, block_tables,
+                     context_lens, max_context_len, window, sm_scale, out,
+                     out_dtype == KVQ_OUT_F32, workspace};
+  return cuda_rc(launch_ragged(a, fmt, *dims, stream));
+}
+
 size_t kvq_decode_workspace_bytes(int32_t batch, int32_t max_context_len, int32_t partition_tokens,
                                   kvq_fmt fmt, const kvq_dims* dims) {
   DecodePlan plan;
@@ -203,8 +320,12 @@ int64_t kvq_get_wait_limit(void) { return decode_wait_limit(); }
 
 int kvq_device_error(uint32_t* flags, int clear) {
   if (!flags) return KVQ_ERR_ARG;
-  const int e = read_device_error(flags, clear);
-  if (e != 0) return KVQ_ERR_CUDA;
+  if (cudaDeviceSynchronize() != cudaSuccess) return KVQ_ERR_CUDA;
+  uint32_t a = 0, b = 0, c = 0;
+  if (read_kernels_error(&a, clear) != 0 || read_ops_error(&b, clear) != 0 ||
+      read_ragged_error(&c, clear) != 0)
+    return KVQ_ERR_CUDA;
+  *flags = a | b | c;
   return *flags ? KVQ_ERR_DEVICE : KVQ_OK;
 }
 

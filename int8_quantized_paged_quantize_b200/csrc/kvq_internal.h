@@ -94,7 +94,47 @@ int launch_prefill_partial(const void* q, int32_t B, const void* kc, const void*
 int launch_decode_merge(int32_t B, const int32_t* ctx, int32_t max_ctx, void* out, bool out_f32,
                         const void* ws, const DecodePlan& plan, const kvq_dims& d, void* stream,
                         int rows_per_count = 0);
-int read_device_error(uint32_t* flags, int clear);
+// The write with rotary embedding: strided rows, positions and angles.
+struct RopeArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  const int32_t* positions;
+  const float* cos_sin;                   // [max_position][rotary_dim]
+  int32_t max_position, rotary_dim;
+  bool interleaved;
+  void* q_out;
+};
+int launch_append_rope(const RopeArgs& a, const int64_t* slots, int32_t T, void* kc, void* vc,
+                       void* ks, void* vs, kvq_fmt fmt, const kvq_dims& d, void* stream);
+// The read-back of token runs.
+struct ReadArgs {
+  const void *kc, *vc, *ks, *vs;
+  const int32_t *tables, *starts, *cu;
+  int32_t n_seqs, total;
+  void *k_out, *v_out;
+  bool out_f32;
+};
+int launch_read(const ReadArgs& a, kvq_fmt fmt, const kvq_dims& d, void* stream);
+// Attention of ragged chunks.
+struct RaggedArgs {
+  const void* q;
+  int64_t q_stride;                       // elements between tokens
+  const int32_t* cu_q;
+  int32_t n_seqs, total_q;
+  const void *kc, *vc, *ks, *vs;
+  const int32_t *tables, *ctx;
+  int32_t max_ctx, window;
+  float sm_scale;
+  void* out;
+  bool out_f32;
+  void* workspace;
+};
+size_t ragged_workspace(int32_t total_q, const kvq_dims& d);
+int launch_ragged(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d, void* stream);
+// The error words of the translation units with kernels (the device is idle).
+int read_kernels_error(uint32_t* flags, int clear);
+int read_ops_error(uint32_t* flags, int clear);
+int read_ragged_error(uint32_t* flags, int clear);
 int launch_kivi_decode(const void* q, int32_t B, const void* kc, const void* vc, const void* km,
                        const void* vm, const int32_t* tables, const int32_t* qlens,
                        int32_t max_qlen, const void* rk, const void* rv,

@@ -1,0 +1,1200 @@
+// Attention of ragged chunks of new tokens over the paged quantized cache
+// (kvq_ragged_attn): sequence b brings n_b new tokens, the last n_b of its
+// cached context, and row i of them, at position p = ctx_b - n_b + i, attends
+// the cached tokens t <= p (with a window w: p - w < t <= p):
+//   out = sum_t softmax_t(sm_scale q . K_t) V_t, K and V as the codes stand for.
+//
+// A flash-attention loop on the 5th-generation tensor cores. A CTA takes a
+// block of up to 256 query rows of one (sequence, KV head) (rows of the G query
+// heads that share the head, token by token) and walks the cached tokens in
+// steps of 64:
+//   S[128 x 64] = Q . K^T      Q in shared memory, K codes expanded to f16
+//   P = 2^(S a + b - m)        FP32 registers, one row a thread
+//   O[128 x D] += (P sv) . V   P sv as f16 in tensor memory, V codes as f16
+// with a, sv the token's K and V scales (INT8: the zero points add b to the
+// score and leave a correction of O). The 8-bit codes are exact in f16, the
+// query is exact in f16 after a power-of-two scaling of its row (the elements
+// below 2^-29 of the largest aside), and the products accumulate in FP32: the
+// scores are those of the dequantized cache up to FP32 rounding. A BF16 cache
+// is multiplied as it is stored. Running maximum, sum and O are FP32.
+// The weights P sv are rounded to 11 bits (BF16 cache: 8) for a BF16 output,
+// whose own rounding is to 8; for an FP32 output they are kept to 22 (16) bits
+// as two parts (HP), and with static INT8 scales, where the K scale of each
+// channel multiplies the query, the query as two f16 parts.
+//
+// The two halves of the CTA work on different products at the same time, so
+// that one's exponentials cover the other's matrix products: slot A and slot B
+// have their own S, P and O in tensor memory and four softmax warps each. A
+// block of more than 128 rows puts its first 128 rows in slot A and the others
+// in slot B, and every step runs in both (the codes are expanded once for 256
+// rows). A block of at most 128 rows runs its even steps in slot A and its odd
+// ones in slot B, over the same rows, and joins the two at its end.
+//
+// The online softmax moves a row's reference m only when the largest weight a
+// step could give, the largest score times the step's largest V scale, passes
+// 2^8 relative to it (O is then rescaled in tensor memory). That also keeps
+// P sv inside the range of f16.
+//
+// Work split: see kvq_ragged_plan.h. A block that lies in one CTA's share is
+// finished there; the first and the last of a share may be pieces, whose
+// (m, l, O) go to the workspace (two places a CTA) for ragged_merge_kernel.
+//
+// 14 warps per CTA, one CTA per SM:
+//   0       producer: 1-D bulk copies of 4 K and 4 V pages a step into a ring
+//           of raw stages, the scales beside them by plain loads
+//   1       tensor memory, and one thread that issues the products
+//   2..5    softmax of slot A (thread = row = TMEM lane), 6..9 of slot B
+//   10..13  converters: codes of a step to f16 (BF16 cache: none), V of tokens
+//           past the end zeroed, the scales as FP32 column factors
+//
+// A token whose V row holds a NaN or an infinity (with a per-token scale: whose
+// V scale is one) makes every channel of the rows that attend it NaN and leaves
+// the other rows alone: its V is zeroed in the operand, where 0 x NaN would
+// reach every row, and the rows that attend it get a NaN sum.
+//
+// Every wait is bounded, as in the other attention kernels: on expiry the CTA
+// stops issuing, drains, writes NaN and returns.
+#pragma once
+
+#include "kvq_common.cuh"
+#include "kvq_prefill.cuh"
+#include "kvq_ragged_plan.h"
+
+namespace kvq {
+
+template <int D, int FMT, bool HP>
+struct RgCfg {
+  static constexpr bool BF = FMT == KVQ_BF16;
+  static constexpr bool F8 = FMT == KVQ_FP8_E4M3 || FMT == KVQ_FP8_E5M2;
+  static constexpr bool SI = FMT == KVQ_INT8_CHANNEL;            // static per channel / per tensor
+  static constexpr bool ZP = FMT == KVQ_INT8_ASYM;
+  static constexpr int E = BF ? 2 : 1;
+  static constexpr int PAGE = kBlockSize * D * E;                // raw page bytes
+  static constexpr int MV = F8 ? 1 : (ZP ? 2 : 0);
+  static constexpr int METAB = kBlockSize * MV * 2;              // raw scale bytes of a page
+  static constexpr int ST = kRgStep, PPS = kRgStep / kBlockSize; // tokens, pages per step
+  static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
+  static constexpr int RPB = QP == 2 ? 128 : 256;                // rows per block
+  static constexpr int PP = HP ? 2 : 1;                          // weight parts
+  static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
+  static constexpr int NC = BF ? NRAW : 3;                       // operand stages
+  static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
+  static constexpr int CMETA = 4 * ST * 4 + 16;                  // a, b, sv, zv per token; 2 log2 of max sv
+  static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
+  static constexpr int QBYTES = 128 * D * 2;
+  static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
+  static constexpr uint32_t V_LBO = 16 * D, V_SBO = 128;
+  static constexpr uint32_t Q_LBO = 128, Q_SBO = 16 * D;
+  // tensor memory: O of slots A and B, then S and P of each
+  static constexpr int COL_O = 0, COL_S = 2 * D, COL_P = 2 * D + 128, TMEM_COLS = 512;
+  static constexpr int RSTAGE = 2 * PPS * PAGE;                  // K pages, V pages
+  static constexpr int RMETA = 2 * PPS * METAB;
+  static constexpr int OFF_R = 0;
+  static constexpr int OFF_Q = OFF_R + NRAW * RSTAGE;
+  static constexpr int OFF_C = OFF_Q + 2 * QBYTES;
+  static constexpr int OFF_RM = (OFF_C + NC * CSTAGE + 15) / 16 * 16;
+  static constexpr int OFF_X = OFF_RM + NRAW * RMETA;            // float [16][128]: joining the slots
+  static constexpr int OFF_XS = OFF_X + 16 * 128 * 4;            // float4 [128]: m, l, corr of slot B
+  static constexpr int OFF_BAR = OFF_XS + 128 * 16;
+  static constexpr int NBAR = 2 * NRAW + 2 * NC + 8 + 2;
+  static constexpr int OFF_MASK = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;   // raw page masks [NRAW], then [NC][12]
+  static constexpr int OFF_RED = OFF_MASK + 16 * ((NRAW + 3) / 4) + 48 * NC;
+  static constexpr int OFF_MISC = OFF_RED + 128;
+  static constexpr int USED = OFF_MISC + 48;
+  // one CTA per SM (it takes all tensor memory): never less than half of an SM's shared memory
+  static constexpr int SMEM = (USED < 118 * 1024 ? 118 * 1024 : USED) + 1024;
+  static_assert(OFF_C % 128 == 0 && OFF_Q % 128 == 0 && CSTAGE % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// What describes the batch (device memory) and the shape.
+struct RgBatch {
+  const int32_t* cu;
+  const int32_t* ctx_lens;
+  int B, T, Hk, G, W, max_ctx, window, pos_per_block;
+
+  // sequence b: its new tokens and context; a range or a context that is not
+  // legal counts as empty
+  __device__ __forceinline__ RgSeq seq(int b, int* row0, unsigned* bad) const {
+    const int c0 = cu[b], c1 = cu[b + 1], x = ctx_lens[b];
+    RgSeq s;
+    s.n = c1 - c0;
+    s.ctx = x;
+    unsigned f = 0;
+    if (c0 < 0 || c1 < c0 || c1 > T) {
+      f = KVQ_DEVERR_RANGE;
+      s.n = 0;
+    }
+    if (x < 0 || x > max_ctx || int64_t(x) > int64_t(W) * kBlockSize) {
+      f |= KVQ_DEVERR_CONTEXT;
+      s.ctx = 0;
+    }
+    *row0 = c0;
+    if (bad) *bad = f;
+    return s;
+  }
+};
+
+// Cursor over the pieces of one CTA's share.
+struct RgWalk {
+  RgSeq s;
+  int b, h, k, nb, row0;
+  long long pos, start, end;
+  int first, count, lo, hi, rows;
+  bool done;
+
+  __device__ __forceinline__ void load(const RgBatch& a) {          // the next sequence with rows, from b on
+    nb = 0;
+    while (b < a.B) {
+      s = a.seq(b, &row0, nullptr);
+      nb = rg_blocks(s, a.pos_per_block);
+      if (nb > 0) return;
+      ++b;
+    }
+  }
+  __device__ __forceinline__ int weight() const { return rows > 128 ? 2 : 1; }
+  __device__ __forceinline__ bool item(const RgBatch& a) {
+    rg_block(s, k, a.pos_per_block, a.window, &first, &count);
+    rows = rg_rows(s, k, a.pos_per_block, a.G);
+    return rg_piece(pos, count, weight(), start, end, &lo, &hi);
+  }
+  __device__ __forceinline__ void step(const RgBatch& a) {
+    pos += kRgPiece + (long long)weight() * count;
+    if (++k < nb) return;
+    k = 0;
+    if (++h < a.Hk) return;
+    h = 0;
+    ++b;
+    load(a);
+  }
+  __device__ __forceinline__ void settle(const RgBatch& a) {
+    while (true) {
+      if (pos >= end || nb == 0) {
+        done = true;
+        return;
+      }
+      if (item(a)) {
+        done = false;
+        return;
+      }
+      step(a);
+    }
+  }
+  // P0: cost per KV head of the sequences before b0
+  __device__ __forceinline__ void init(const RgBatch& a, int b0, long long P0, long long start_, long long end_) {
+    b = b0;
+    start = start_;
+    end = end_;
+    load(a);
+    const long long L = rg_cost(s, a.pos_per_block, a.G, a.window);
+    const long long off = start - P0 * a.Hk;
+    h = int(off / L);
+    k = rg_find(s, off - h * L, a.pos_per_block, a.G, a.window);
+    pos = P0 * a.Hk + h * L + rg_prefix(s, k, a.pos_per_block, a.G, a.window);
+    settle(a);
+  }
+  __device__ __forceinline__ void next(const RgBatch& a) {
+    step(a);
+    settle(a);
+  }
+  __device__ __forceinline__ bool whole() const { return lo == 0 && hi == count; }
+};
+
+// A piece's place in the workspace: what the joining kernel has to know.
+struct RgPiece {
+  int valid, last, row0, n, h, k, pad0, pad1;
+};
+static_assert(sizeof(RgPiece) == 32, "layout");
+
+// 1-D bulk copy global -> shared. No L2 hint: the pages of a sequence are read
+// again for its other blocks.
+__device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// 32 lanes x 32 columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+template <int D, int FMT, bool HP>
+__global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
+    const __nv_bfloat16* __restrict__ q, int64_t q_stride, const uint8_t* __restrict__ kc,
+    const uint8_t* __restrict__ vc, const __nv_bfloat16* __restrict__ ks,
+    const __nv_bfloat16* __restrict__ vs, const int32_t* __restrict__ tables, const RgBatch bt, int NB,
+    float qk_scale, int per_tensor, long long wait_limit, void* __restrict__ out_,
+    float* __restrict__ part_o, float* __restrict__ part_ml, RgPiece* __restrict__ pieces, int rows_cap) {
+  using C = RgCfg<D, FMT, HP>;
+  using namespace tc;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int NWARPS = 14;
+
+  uint8_t* raw = smem + C::OFF_R;
+  uint8_t* rmeta = smem + C::OFF_RM;
+  uint8_t* cst = smem + C::OFF_C;
+  uint8_t* qop = smem + C::OFF_Q;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* rfull = bars;                     // [NRAW] producer -> converters
+  uint64_t* rfree = rfull + C::NRAW;          // [NRAW]
+  uint64_t* cfull = rfree + C::NRAW;          // [NC] converters -> MMA, softmax
+  uint64_t* cfree = cfull + C::NC;            // [NC] the step's products have completed
+  uint64_t* sfull = cfree + C::NC;            // [2] S of a slot in tensor memory
+  uint64_t* sfree = sfull + 2;                // [2] S read by the slot's softmax warps
+  uint64_t* pready = sfree + 2;               // [2] P of a slot in tensor memory
+  uint64_t* pvdone = pready + 2;              // [2] the slot's last PV product has completed
+  uint64_t* qready = pvdone + 2;              // the query operand of the next piece
+  uint64_t* drain = qready + 1;
+  volatile uint32_t* rmask = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MASK);
+  // per operand stage: {valid pages}, {not-finite V tokens 0..31}, {.. 32..63} as
+  // each converter warp saw them
+  uint4* cmask = reinterpret_cast<uint4*>(smem + C::OFF_MASK + 16 * ((C::NRAW + 3) / 4));
+  long long* red64 = reinterpret_cast<long long*>(smem + C::OFF_RED);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* misci = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
+  long long* miscll = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);
+
+  // ------------------------------------------------------------ set-up
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NRAW; ++s) {
+      mbar_init(rfull + s, 1);
+      mbar_init(rfree + s, C::BF ? 1 : 128);
+    }
+    for (int j = 0; j < C::NC; ++j) {
+      mbar_init(cfull + j, 128);
+      mbar_init(cfree + j, 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(sfull + j, 1);
+      mbar_init(sfree + j, 128);
+      mbar_init(pready + j, 128);
+      mbar_init(pvdone + j, 1);
+    }
+    mbar_init(qready, 256);
+    mbar_init(drain, 1);
+    for (int j = 0; j < 3 * C::NC; ++j) cmask[j] = make_uint4(0, 0, 0, 0);
+    *abort_flag = 0;
+    misci[0] = -1;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // every argument in device memory is read, and the workspace written, after
+  // the kernel ahead on the stream has finished
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+
+  // ------------------------------------------------------------ the share
+  long long T = 0;                             // cost of the whole list
+  {
+    long long sum = 0;
+    for (int bb = threadIdx.x; bb < bt.B; bb += blockDim.x) {
+      int row0;
+      unsigned bad;
+      const RgSeq s = bt.seq(bb, &row0, &bad);
+      if (bad && blockIdx.x == 0) flag_error(bad);
+      sum += rg_cost(s, bt.pos_per_block, bt.G, bt.window);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red64[warp] = sum;
+    if (threadIdx.x < 2) pieces[2 * blockIdx.x + threadIdx.x].valid = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) T += red64[w];
+    T *= bt.Hk;
+  }
+  const long long N = ll_min((long long)gridDim.x, ll_max(1, T / kRgMinShare));
+  if (T == 0 || blockIdx.x >= N) {             // uniform for the CTA
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
+  const long long start = (blockIdx.x * T) / N, end = ((blockIdx.x + 1) * T) / N;
+  {
+    // the sequence that holds cost position `start`
+    long long run = 0;
+    for (int base = 0; base < bt.B; base += blockDim.x) {
+      const int bb = base + threadIdx.x;
+      long long c = 0;
+      if (bb < bt.B) {
+        int row0;
+        c = rg_cost(bt.seq(bb, &row0, nullptr), bt.pos_per_block, bt.G, bt.window);
+      }
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) red64[warp] = incl;
+      __syncthreads();
+      long long before = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < NWARPS; ++w) {
+        before += w < warp ? red64[w] : 0;
+        total += red64[w];
+      }
+      const long long p0 = run + before + incl - c;
+      if (c > 0 && p0 * bt.Hk <= start && start < (p0 + c) * bt.Hk) {
+        misci[0] = bb;
+        miscll[0] = p0;
+      }
+      run += total;
+      __syncthreads();
+      if (misci[0] >= 0) break;                // uniform
+    }
+  }
+  RgWalk walk;
+  walk.init(bt, misci[0], miscll[0], start, end);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
+    const int sp = lane / CPP, sc = lane % CPP;
+    auto step = [&](RgWalk& w, int& i) {
+      if (w.done) return;
+      if (++i >= w.hi) {
+        do w.next(bt); while (!w.done && w.count == 0);
+        i = w.lo;
+      }
+    };
+    // block id of page `lane` of step i (-2: no page there)
+    auto load_id = [&](const RgWalk& w, int i) -> int {
+      if (lane >= C::PPS || w.done) return -2;
+      const int pg = (w.first + i) * C::PPS + lane;
+      return int64_t(pg) * kBlockSize < w.s.ctx ? tables[int64_t(w.b) * bt.W + pg] : -2;
+    };
+    RgWalk c0 = walk;
+    while (!c0.done && c0.count == 0) c0.next(bt);
+    int i0 = c0.lo;
+    RgWalk c1 = c0;
+    int i1 = i0;
+    step(c1, i1);
+    int id0 = load_id(c0, i0);
+    int issued = 0;
+    for (int u = 0; !c0.done; ++u) {
+      const int s = u % C::NRAW;
+      const uint32_t ph = (u / C::NRAW) & 1;
+      const int id1 = load_id(c1, i1);                     // the next step's block ids, in flight
+      const bool valid = id0 >= 0 && id0 < NB;
+      if (id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
+      const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
+      const int64_t page = int64_t(id0) * bt.Hk + c0.h;
+      uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
+      const bool smine = C::MV > 0 && sp < C::PPS && ((mask >> (sp & 3)) & 1u) != 0u;
+      if constexpr (C::MV > 0) {
+        const int sblk = __shfl_sync(0xffffffffu, id0, sp & 3);
+        if (smine) {
+          const int64_t off = (int64_t(sblk) * bt.Hk + c0.h) * C::METAB + sc * 16;
+          kv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ks) + off));
+          vv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(vs) + off));
+        }
+      }
+      bool ok = true;
+      if (lane == 0) {
+        ok = u < C::NRAW || mbar_wait(rfree + s, ph ^ 1, abort_flag, wait_limit);
+        if (ok) mbar_expect_tx(rfull + s, 2u * uint32_t(__popc(mask)) * uint32_t(C::PAGE));
+      }
+      if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
+      uint8_t* st = raw + s * C::RSTAGE;
+      if (valid) {
+        bulk_g2s_keep(st + lane * C::PAGE, kc + page * C::PAGE, C::PAGE, rfull + s);
+        bulk_g2s_keep(st + (C::PPS + lane) * C::PAGE, vc + page * C::PAGE, C::PAGE, rfull + s);
+      }
+      if constexpr (C::MV > 0) {
+        if (smine) {
+          uint8_t* m = rmeta + s * C::RMETA;
+          *reinterpret_cast<uint4*>(m + sp * C::METAB + sc * 16) = kv;
+          *reinterpret_cast<uint4*>(m + (C::PPS + sp) * C::METAB + sc * 16) = vv;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        rmask[s] = mask;
+        mbar_arrive(rfull + s);
+      }
+      issued = u + 1;
+      c0 = c1;
+      i0 = i1;
+      id0 = id1;
+      step(c1, i1);
+    }
+    if (lane == 0 && *abort_flag) {
+      // the copies already issued land before the CTA's shared memory goes away
+      volatile int no_abort = 0;
+      for (int u = issued > C::NRAW ? issued - C::NRAW : 0; u < issued; ++u)
+        mbar_wait(rfull + u % C::NRAW, (u / C::NRAW) & 1, &no_abort, kMmaWaitLimitCycles);
+    }
+  } else if (warp >= 10) {
+    // ---------------------------------------------------------- converters
+    const int ct = threadIdx.x - 320;                      // 0 .. 127
+    bool ok = true;
+    int u = 0;
+    for (RgWalk w = walk; !w.done; w.next(bt)) {
+      for (int i = w.lo; i < w.hi; ++i, ++u) {
+        const int s = u % C::NRAW, cs = u % C::NC;
+        if (ok) ok = mbar_wait(rfull + s, (u / C::NRAW) & 1, abort_flag, wait_limit);
+        if (ok && !C::BF && u >= C::NC) ok = mbar_wait(cfree + cs, (u / C::NC - 1) & 1, abort_flag, wait_limit);
+        ok = __all_sync(0xffffffffu, ok);                  // what follows votes and reduces over the warp
+        const uint32_t pm = rmask[s];
+        const int tok0 = (w.first + i) * C::ST;
+        uint8_t* rk = raw + s * C::RSTAGE;
+        uint8_t* rv = rk + C::PPS * C::PAGE;
+        uint8_t* cb = cst + cs * C::CSTAGE;
+        uint32_t* cmw = reinterpret_cast<uint32_t*>(cmask + 3 * cs);
+        // tokens of page p that hold cache entries
+        auto nvalid = [&](int p) -> int {
+          if (((pm >> p) & 1u) == 0u) return 0;
+          return max(0, min(16, w.s.ctx - (tok0 + 16 * p)));
+        };
+        if (ok) {
+          if constexpr (C::BF) {
+            // V as it is stored: tokens that hold nothing, and tokens with a NaN
+            // or an infinity, are zeroed
+            if (ct == 0) cmw[0] = pm;
+            uint32_t bad0 = 0u, bad1 = 0u;
+            constexpr int NIT = C::PPS * 2 * D / 128;
+#pragma unroll 4
+            for (int it = 0; it < NIT; ++it) {
+              const int x = ct + 128 * it;                 // chunk: 8 tokens of a channel
+              const int p = x / (2 * D), o8 = ((x / D) & 1) * 8;
+              const int keep = max(0, min(8, nvalid(p) - o8));
+              uint4* ch = reinterpret_cast<uint4*>(rv + x * 16);
+              const uint4 c4 = *ch;
+              uint32_t wv[4] = {c4.x, c4.y, c4.z, c4.w};
+              uint32_t mx = 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx = vmax_u16x2(mx, wv[e] & 0x7fff7fffu);
+              const bool wild = max(mx & 0xffffu, mx >> 16) >= 0x7f80u;
+              if (keep == 8 && !wild) continue;
+              uint32_t bad = 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t m = 0u;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t v16 = (wv[e] >> (16 * z)) & 0x7fffu;
+                  const int t = 2 * e + z;
+                  if (t < keep && v16 < 0x7f80u) m |= 0xffffu << (16 * z);
+                  if (t < keep && v16 >= 0x7f80u) bad |= 1u << t;
+                }
+                wv[e] &= m;
+              }
+              *ch = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+              bad <<= (p & 1) * 16 + o8;
+              if (p < 2) bad0 |= bad;
+              else bad1 |= bad;
+            }
+            bad0 = __reduce_or_sync(0xffffffffu, bad0);
+            bad1 = __reduce_or_sync(0xffffffffu, bad1);
+            if (lane == 0) {
+              cmw[4 + (ct >> 5)] = bad0;
+              cmw[8 + (ct >> 5)] = bad1;
+            }
+          } else {
+            uint8_t* ck = cb;
+            uint8_t* cv = cb + C::PPS * C::CPAGE;
+            float* cm = reinterpret_cast<float*>(cb + 2 * C::PPS * C::CPAGE);
+            const uint8_t* mk = rmeta + s * C::RMETA;
+            const uint8_t* mv = mk + C::PPS * C::METAB;
+            // every raw chunk is loaded before any converted one is stored
+            constexpr int NIT = C::PPS * D / 128;
+            uint4 kraw[NIT], vraw[NIT];
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              const int x = ct + 128 * it;                 // K: 16 channels of a token; V: 16 tokens of a channel
+              kraw[it] = *reinterpret_cast<const uint4*>(rk + x * 16);
+              vraw[it] = *reinterpret_cast<const uint4*>(rv + x * 16);
+            }
+            // per-token column factors: score = S a + b qsum, weight P sv, V zero point zv
+            if (ct < C::ST) {
+              const int p = ct >> 4, tk = ct & 15;
+              float a = 0.f, b = 0.f, sv = 0.f, zv = 0.f;
+              bool wild = false;
+              if (tk < nvalid(p)) {
+                if constexpr (C::F8) {
+                  a = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + p * C::METAB + tk * 2)) * qk_scale;
+                  sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + p * C::METAB + tk * 2));
+                } else if constexpr (C::ZP) {
+                  const __nv_bfloat162 km = *reinterpret_cast<const __nv_bfloat162*>(mk + p * C::METAB + tk * 4);
+                  const __nv_bfloat162 vm = *reinterpret_cast<const __nv_bfloat162*>(mv + p * C::METAB + tk * 4);
+                  a = __low2float(km) * qk_scale;
+                  b = -__low2float(km) * __high2float(km) * qk_scale;
+                  sv = __low2float(vm);
+                  zv = __high2float(vm);
+                } else {
+                  a = qk_scale;
+                  sv = 1.f;
+                }
+                wild = !(fabsf(sv) < INFINITY);
+                if (wild) sv = zv = 0.f;
+              }
+              cm[ct] = a;
+              cm[C::ST + ct] = b;
+              cm[2 * C::ST + ct] = sv;
+              cm[3 * C::ST + ct] = zv;
+              const float top = warp_max_f32(fabsf(sv));
+              const unsigned wm = __ballot_sync(0xffffffffu, wild);
+              if ((ct & 31) == 0) {
+                cm[4 * C::ST + (ct >> 5)] = top > 0.f ? fmaxf(__log2f(top), -64.f) : -64.f;
+                cmw[ct < 32 ? 4 : 9] = wm;
+                if (ct == 0) cmw[0] = pm;
+              }
+            }
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              const int x = ct + 128 * it;
+              const int p = x / D, k = x % D;
+              const int g = k / (D / 2), rem = k % (D / 2), c = rem >> 3, tt = rem & 7;
+              uint4 o0, o1;
+              codes16_to_f16<FMT>(kraw[it], o0, o1);
+              uint8_t* dst = ck + p * C::CPAGE + g * 16 * D + (2 * c) * 128 + tt * 16;
+              *reinterpret_cast<uint4*>(dst) = o0;
+              *reinterpret_cast<uint4*>(dst + 128) = o1;
+            }
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+              const int x = ct + 128 * it;
+              const int p = x / D, d = x % D;              // p is the same for a whole warp
+              const int nv = nvalid(p);
+              uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;
+              if constexpr (C::MV > 0) {                   // tokens whose scale is finite
+                const uint16_t sb = *reinterpret_cast<const uint16_t*>(mv + p * C::METAB + (lane & 15) * 2 * C::MV);
+                keep &= ~__ballot_sync(0xffffffffu, lane < 16 && (sb & 0x7fffu) >= 0x7f80u);
+              }
+              uint4 o0, o1;
+              codes16_to_f16<FMT>(vraw[it], o0, o1);
+              uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+              if (keep != 0xffffu) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  wv[e] &= ((keep >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((keep >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+              }
+              uint8_t* pg = cv + p * C::CPAGE;
+              *reinterpret_cast<uint4*>(pg + d * 16) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+              *reinterpret_cast<uint4*>(pg + (D + d) * 16) = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(cfull + cs);
+        if constexpr (!C::BF) mbar_arrive(rfree + s);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
+      constexpr uint32_t id_pv = idesc_f16(D, C::BF);
+      const uint32_t qaddr = smem_u32(qop), raddr = smem_u32(raw), caddr = smem_u32(cst);
+      bool ok = true;
+      int u = 0, pc = 0;
+      uint32_t cnt[2] = {0, 0};                            // steps of each slot so far
+      // a slot's PV product that waits for its P
+      int pend[2] = {-1, -1};                              // its step
+      bool pend_first[2] = {false, false}, pend_free[2] = {false, false};
+      auto issue_pv = [&](int x) -> bool {
+        if (pend[x] < 0) return true;
+        if (!mbar_wait(pready + x, (cnt[x] - 1) & 1, abort_flag, wait_limit)) return false;
+        tc_fence_after();
+        const int up = pend[x];
+        const uint32_t vb = C::BF ? raddr + (up % C::NRAW) * C::RSTAGE + C::PPS * C::PAGE
+                                  : caddr + (up % C::NC) * C::CSTAGE + C::PPS * C::CPAGE;
+#pragma unroll
+        for (int j = 0; j < C::PP; ++j)
+#pragma unroll
+          for (int kk = 0; kk < C::PPS; ++kk)
+            mma_f16_ts(tmem + C::COL_O + x * D, tmem + C::COL_P + x * 64 + j * 32 + 8 * kk,
+                       sdesc_plain(vb + kk * C::CPAGE, C::V_LBO, C::V_SBO), id_pv,
+                       (pend_first[x] && j == 0 && kk == 0) ? 0u : 1u);
+        mma_commit(pvdone + x);
+        if (pend_free[x]) {
+          // the step's last product: its stage is free
+          if constexpr (C::BF) mma_commit(rfree + up % C::NRAW);
+          else mma_commit(cfree + up % C::NC);
+        }
+        pend[x] = -1;
+        return true;
+      };
+      auto issue_qk = [&](int x, int step, bool first, bool frees, int qx) -> bool {
+        if (cnt[x] > 0 && !mbar_wait(sfree + x, (cnt[x] - 1) & 1, abort_flag, wait_limit)) return false;
+        tc_fence_after();
+        const uint32_t kb = C::BF ? raddr + (step % C::NRAW) * C::RSTAGE : caddr + (step % C::NC) * C::CSTAGE;
+#pragma unroll
+        for (int qp = 0; qp < C::QP; ++qp)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss<0>(tmem + C::COL_S + x * 64,
+                      sdesc_plain(qaddr + (qp + qx) * C::QBYTES + kk * 256, C::Q_LBO, C::Q_SBO),
+                      sdesc_plain(kb + kk * 256, C::K_LBO, C::K_SBO), id_s, (qp | kk) ? 1u : 0u);
+        mma_commit(sfull + x);
+        // the PV product of the slot's step before
+        if (!issue_pv(x)) return false;
+        pend[x] = step;
+        pend_first[x] = first;
+        pend_free[x] = frees;
+        ++cnt[x];
+        return true;
+      };
+      for (RgWalk w = walk; ok && !w.done; w.next(bt)) {
+        if (w.count == 0) continue;
+        const bool two = w.rows > 128;
+        ok = mbar_wait(qready, pc & 1, abort_flag, wait_limit);
+        ++pc;
+        for (int i = w.lo; ok && i < w.hi; ++i, ++u) {
+          ok = mbar_wait(cfull + u % C::NC, (u / C::NC) & 1, abort_flag, wait_limit);
+          if (!ok) break;
+          if (two) {
+            ok = issue_qk(0, u, i == w.lo, false, 0) && issue_qk(1, u, i == w.lo, true, 1);
+          } else {
+            const int x = (i - w.lo) & 1;
+            ok = issue_qk(x, u, i - w.lo < 2, true, 0);
+          }
+        }
+        // in the order of the steps, so that stages come free in order
+        if (ok) {
+          const int a = pend[1] >= 0 && (pend[0] < 0 || pend[1] < pend[0]) ? 1 : 0;
+          ok = issue_pv(a) && issue_pv(a ^ 1);
+        }
+      }
+      // every product issued completes before tensor memory is released
+      volatile int no_abort = 0;
+      mma_commit(drain);
+      mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax warps
+    const int quarter = warp & 3;
+    const int x = (warp - 2) >> 2;                         // slot
+    const int r = quarter * 32 + lane;                     // row of the slot, TMEM lane
+    const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+    const uint32_t t_o = tmem + lane_base + C::COL_O + x * D;
+    const uint32_t t_s = tmem + lane_base + C::COL_S + x * 64;
+    const uint32_t t_p = tmem + lane_base + C::COL_P + x * 64;
+    float* xch = reinterpret_cast<float*>(smem + C::OFF_X);              // [16][128]
+    float4* xsum = reinterpret_cast<float4*>(smem + C::OFF_XS);          // [128]
+    const int pair_bar = 2 + quarter;                      // the two warps of this lane quarter
+    const int gshift = __ffs(bt.G) - 1;
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {  // tcgen05.ld / st are warp-wide
+      if (ok) ok = mbar_wait(bar, parity, abort_flag, wait_limit);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    // this thread's row of a block: the block row, its token of the sequence's new ones
+    auto block_row = [&](const RgWalk& w) -> int { return w.rows > 128 ? x * 128 + r : r; };
+    auto token_of = [&](const RgWalk& w, int rr) -> int { return w.k * bt.pos_per_block + (rr >> gshift); };
+    auto head_of = [&](const RgWalk& w, int rr) -> int { return (w.h << gshift) + (rr & (bt.G - 1)); };
+
+    // The query row of a piece into the operand (K-major 8-row groups of
+    // 16-byte chunks). `down` takes S back to the row's units, qsum is the sum of
+    // the operand's values (the zero-point term). With one block of rows for
+    // both slots, slot A's warps write it.
+    auto store_q = [&](const RgWalk& w, float& down, float& qsum) {
+      down = 1.f;
+      qsum = 0.f;
+      const bool two = w.rows > 128;
+      const int rr = block_row(w);
+      const bool have = rr < w.rows, wr = two || x == 0;
+      uint4 c[D / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(
+          q + int64_t(w.row0 + (have ? token_of(w, rr) : 0)) * q_stride + int64_t(head_of(w, rr)) * D);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) c[i] = have ? src[i] : make_uint4(0, 0, 0, 0);
+      uint8_t* row = qop + (two ? x : 0) * C::QBYTES + (r >> 3) * C::Q_SBO + (r & 7) * 16;
+      if constexpr (C::BF) {
+        if (wr) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(row + i * C::Q_LBO) = c[i];
+        }
+      } else {
+        // static INT8: q times the K scale of the channel
+        auto scale = [&](int d) -> float {
+          if constexpr (C::SI) return __bfloat162float(ks[per_tensor ? 0 : w.h * D + d]);
+          return 1.f;
+        };
+        float amax = 0.f;
+        if constexpr (C::SI) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(v[e]) * scale(8 * i + 2 * e)),
+                                       fabsf(bf16_hi(v[e]) * scale(8 * i + 2 * e + 1))));
+          }
+        } else {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            m = vmax_u16x2(m, c[i].x & 0x7fff7fffu);
+            m = vmax_u16x2(m, c[i].y & 0x7fff7fffu);
+            m = vmax_u16x2(m, c[i].z & 0x7fff7fffu);
+            m = vmax_u16x2(m, c[i].w & 0x7fff7fffu);
+          }
+          amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+        }
+        // power-of-two scaling: the largest element lands in [2^14, 2^15)
+        int e2 = 0;
+        if (amax > 0.f && amax < INFINITY) e2 = 14 - ilogbf(amax);
+        e2 = max(-100, min(100, e2));
+        const float up = __int_as_float((127 + e2) << 23);
+        down = __int_as_float((127 - e2) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = bf16_lo(v[e]) * scale(8 * i + 2 * e) * up;
+            const float b = bf16_hi(v[e]) * scale(8 * i + 2 * e + 1) * up;
+            const __half2 h2 = __floats2half2_rn(a, b);
+            hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            if constexpr (C::QP == 2) {
+              const __half2 l2 = __floats2half2_rn(a - __low2float(h2), b - __high2float(h2));
+              lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
+            }
+            if constexpr (C::ZP) qsum += __low2float(h2) + __high2float(h2);
+          }
+          if (wr) {
+            *reinterpret_cast<uint4*>(row + i * C::Q_LBO) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (C::QP == 2)
+              *reinterpret_cast<uint4*>(row + C::QBYTES + i * C::Q_LBO) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
+    OutT* out = static_cast<OutT*>(out_);
+    auto store_row16 = [&](OutT* dst, const float (&o)[16]) {
+      if constexpr (HP) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {
+        uint32_t wv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+          wv[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+      }
+    };
+    // blocks in which no row attends anything: zero rows
+    auto skip_empty = [&](RgWalk& w) {
+      while (!w.done && w.count == 0) {
+        const int rr = block_row(w);
+        if (rr < w.rows && (w.rows > 128 || x == 0)) {
+          OutT* dst = out + (int64_t(w.row0 + token_of(w, rr)) * (bt.Hk << gshift) + head_of(w, rr)) * D;
+          const float z[16] = {};
+          for (int c = 0; c < D / 16; ++c) store_row16(dst + 16 * c, z);
+        }
+        w.next(bt);
+      }
+    };
+
+    RgWalk pw = walk;
+    skip_empty(pw);
+    float down = 1.f, qsum = 0.f;
+    if (!pw.done) {
+      store_q(pw, down, qsum);
+      mbar_arrive(qready);
+    }
+    int u0 = 0;                                            // the piece's first step
+    uint32_t cnt = 0, cnt_other = 0;                       // steps of this slot and of the other so far
+    while (!pw.done) {
+      const bool two = pw.rows > 128;
+      const int rr = block_row(pw);
+      const bool row_ok = rr < pw.rows;
+      const bool active = __any_sync(0xffffffffu, row_ok);
+      const int nsteps = pw.hi - pw.lo;
+      const int p = pw.s.ctx - pw.s.n + token_of(pw, rr);
+      // tokens lo_t <= t < lim are attended; rows past the block's see everything
+      // (nothing of them is written)
+      const int lim = row_ok ? max(0, p + 1) : INT_MAX;
+      const int lo_t = row_ok && bt.window > 0 ? max(0, p + 1 - bt.window) : 0;
+      float m_run = -INFINITY, l = 0.f, corr = 0.f;
+      bool any_step = false;
+      for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
+        const int u = u0 + i, ck = u % C::NC;
+        wait_all(cfull + ck, (u / C::NC) & 1);
+        wait_all(sfull + x, cnt & 1);
+        tc_fence_after();
+        if (!active) {
+          mbar_arrive(sfree + x);
+          if (cnt > 0) wait_all(pvdone + x, (cnt - 1) & 1);
+          mbar_arrive(pready + x);
+          ++cnt;
+          continue;
+        }
+        uint32_t sr[C::ST];
+        if (ok) {
+          tmem_ld32(t_s, sr);
+          tmem_ld32(t_s + 32, sr + 32);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::ST; ++c) sr[c] = 0u;
+        }
+        tc_fence_before();
+        mbar_arrive(sfree + x);
+        const float* cm = reinterpret_cast<const float*>(cst + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
+        const uint32_t pages_ok = cmask[3 * ck].x;
+        const uint4 wl = cmask[3 * ck + 1], wh = cmask[3 * ck + 2];
+        const uint32_t wild0 = wl.x | wl.y | wl.z | wl.w, wild1 = wh.x | wh.y | wh.z | wh.w;
+        const int t0 = (pw.first + pw.lo + i) * C::ST;
+        const bool full = __all_sync(0xffffffffu, t0 >= lo_t && t0 + C::ST <= lim && pages_ok == 0xFu &&
+                                                      (wild0 | wild1) == 0u);
+        // scores in the operand's units (times `down`: base-2 scores), in place of S
+        float2* x2 = reinterpret_cast<float2*>(sr);
+        const float2* a2 = reinterpret_cast<const float2*>(cm);
+        const float2* b2 = reinterpret_cast<const float2*>(cm + C::ST);
+        const float2 qs2 = make_float2(qsum, qsum), k2 = make_float2(qk_scale, qk_scale);
+#pragma unroll
+        for (int k = 0; k < C::ST / 2; ++k) {
+          const float2 sv_ = make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
+          if constexpr (C::BF || C::SI) x2[k] = __fmul2_rn(sv_, k2);
+          else if constexpr (C::ZP) x2[k] = __ffma2_rn(sv_, a2[k], __fmul2_rn(b2[k], qs2));
+          else x2[k] = __fmul2_rn(sv_, a2[k]);
+        }
+        bool wild = false;
+        if (!full) {
+          // the tokens this row attends, as bits
+          auto low = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; };
+          uint64_t vis = low(lim - t0) & ~low(lo_t - t0);
+#pragma unroll
+          for (int pg = 0; pg < C::PPS; ++pg)
+            if (((pages_ok >> pg) & 1u) == 0u) vis &= ~(0xffffull << (16 * pg));
+          const uint32_t v0 = uint32_t(vis), v1 = uint32_t(vis >> 32);
+          wild = ((v0 & wild0) | (v1 & wild1)) != 0u;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!((v0 >> c) & 1u)) sr[c] = 0xff800000u;
+            if (!((v1 >> c) & 1u)) sr[32 + c] = 0xff800000u;
+          }
+        }
+        float mt = -INFINITY;
+        {
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C::ST; k += 4) {
+            m0 = fmaxf(m0, __uint_as_float(sr[k]));
+            m1 = fmaxf(m1, __uint_as_float(sr[k + 1]));
+            m2 = fmaxf(m2, __uint_as_float(sr[k + 2]));
+            m3 = fmaxf(m3, __uint_as_float(sr[k + 3]));
+          }
+          mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * down;
+        }
+        if constexpr (C::F8 || C::ZP) mt += fmaxf(cm[4 * C::ST], cm[4 * C::ST + 1]);
+        float alpha = 1.f;
+        if (mt > m_run + 8.f) {
+          if (m_run != -INFINITY) {
+            alpha = exp2f(m_run - mt);
+            l *= alpha;
+            corr *= alpha;
+          }
+          m_run = mt;
+        }
+        const float mref = m_run == -INFINITY ? 0.f : m_run;
+        const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
+        if (rescale) {
+          wait_all(pvdone + x, (cnt - 1) & 1);
+          tc_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t ov[16];
+              tmem_ld16(t_o + 16 * c, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st16(t_o + 16 * c, ov);
+            }
+            tmem_st_wait();
+          }
+        }
+        // weights, 32 tokens at a time, as pairs of 16-bit values
+        const float2 dn2 = make_float2(down, down), nm2 = make_float2(-mref, -mref);
+        const float2* sv2 = reinterpret_cast<const float2*>(cm + 2 * C::ST);
+        const float2* zv2 = reinterpret_cast<const float2*>(cm + 3 * C::ST);
+        float2 ls2 = make_float2(0.f, 0.f), cz2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int kk = 16 * hf + k;
+            const float2 e = __ffma2_rn(x2[kk], dn2, nm2);
+            const float2 p2 = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
+            ls2 = __fadd2_rn(ls2, p2);
+            float2 wv = p2;
+            if constexpr (C::F8 || C::ZP) wv = __fmul2_rn(p2, sv2[kk]);
+            float2 hv;
+            if constexpr (C::BF) {
+              const __nv_bfloat162 b16 = __floats2bfloat162_rn(wv.x, wv.y);
+              ph[k] = *reinterpret_cast<const uint32_t*>(&b16);
+              hv = make_float2(bf16_lo(ph[k]), bf16_hi(ph[k]));
+            } else {
+              const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
+              ph[k] = *reinterpret_cast<const uint32_t*>(&f16);
+              hv = __half22float2(f16);
+            }
+            if constexpr (C::PP == 2) {
+              const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
+              if constexpr (C::BF) {
+                const __nv_bfloat162 b16 = __floats2bfloat162_rn(rest.x, rest.y);
+                pl[k] = *reinterpret_cast<const uint32_t*>(&b16);
+              } else {
+                const __half2 f16 = __floats2half2_rn(rest.x, rest.y);
+                pl[k] = *reinterpret_cast<const uint32_t*>(&f16);
+                if constexpr (C::ZP) hv = __fadd2_rn(hv, __half22float2(f16));
+              }
+            }
+            if constexpr (C::ZP) cz2 = __ffma2_rn(hv, zv2[kk], cz2);
+          }
+          // the last product has read P
+          if (hf == 0 && cnt > 0 && !rescale) {
+            wait_all(pvdone + x, (cnt - 1) & 1);
+            tc_fence_after();
+          }
+          if (ok) {
+            tmem_st16(t_p + 16 * hf, ph);
+            if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 16 * hf, pl);
+          }
+        }
+        l += ls2.x + ls2.y;
+        corr += cz2.x + cz2.y;
+        if (wild) l = __int_as_float(0x7fc00000);
+        if (ok) tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(pready + x);
+        ++cnt;
+        any_step = true;
+      }
+      if (!active) any_step = (two ? 0 : x) < nsteps;
+      cnt_other += two ? nsteps : (x ? (nsteps + 1) / 2 : nsteps / 2);
+      u0 += nsteps;
+
+      // the next piece's query, once the products that read this one's have completed
+      RgWalk nxt = pw;
+      nxt.next(bt);
+      skip_empty(nxt);
+      float down_n = 1.f, qsum_n = 0.f;
+      if (!nxt.done) {
+        if (!two && x == 0 && nsteps > 1) wait_all(sfull + 1, (cnt_other - 1) & 1);
+        store_q(nxt, down_n, qsum_n);
+        mbar_arrive(qready);
+      }
+
+      // ---- the piece's end: O of the last step
+      if (any_step) wait_all(pvdone + x, (cnt - 1) & 1);
+      tc_fence_after();
+      bool good = __all_sync(0xffffffffu, ok && !*abort_flag);
+      float ma = 1.f, mb = 0.f;                            // O = ma O_A + mb O_B (one block of rows)
+      if (!two && active) {
+        if (x == 1) {
+          xsum[r] = make_float4(any_step ? m_run : -INFINITY, any_step ? l : 0.f, any_step ? corr : 0.f, good ? 1.f : 0.f);
+        }
+        named_bar_sync(pair_bar, 64);
+        if (x == 0) {
+          const float4 o = xsum[r];
+          good = __all_sync(0xffffffffu, good && o.w != 0.f);
+          const float m = fmaxf(m_run, o.x);
+          const float mr = m == -INFINITY ? 0.f : m;
+          ma = exp2f(m_run - mr);
+          mb = exp2f(o.x - mr);
+          l = l * ma + o.y * mb;
+          corr = corr * ma + o.z * mb;
+          m_run = m;
+        }
+      }
+      if (active) {
+        const bool whole = pw.whole();
+        const int slot = pw.lo == 0 ? 1 : 0;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t orow = int64_t(pw.row0 + (row_ok ? token_of(pw, rr) : 0)) * (bt.Hk << gshift) + head_of(pw, rr);
+        const int64_t prow = (int64_t(blockIdx.x) * 2 + slot) * rows_cap + rr;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t ov[16];
+          const bool have = good && any_step;
+          if (have) {
+            tmem_ld16(t_o + 16 * c, ov);
+            tmem_ld_wait();
+          }
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = have ? __uint_as_float(ov[e]) : 0.f;
+          if (!two) {
+            if (x == 1) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) xch[e * 128 + r] = o[e];
+            }
+            named_bar_sync(pair_bar, 64);
+            if (x == 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = o[e] * ma + xch[e * 128 + r] * mb;
+            }
+            named_bar_sync(pair_bar, 64);
+          }
+          if (row_ok && (two || x == 0)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float y = o[e] - corr;
+              if constexpr (C::SI) y *= __bfloat162float(vs[per_tensor ? 0 : pw.h * D + 16 * c + e]);
+              if (whole) y *= inv;
+              o[e] = good ? y : __int_as_float(0x7fc00000);
+            }
+            if (whole) {
+              store_row16(out + orow * D + 16 * c, o);
+            } else {
+              float* po = part_o + prow * D + 16 * c;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(po + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+        }
+        if (!whole && (two || x == 0)) {
+          if (row_ok)
+            *reinterpret_cast<float2*>(part_ml + prow * 2) =
+                good ? make_float2(m_run, l) : make_float2(INFINITY, __int_as_float(0x7fc00000));
+          if (x == 0 && r == 0) {
+            RgPiece pc;
+            pc.valid = 1;
+            pc.last = pw.hi == pw.count;
+            pc.row0 = pw.row0;
+            pc.n = pw.s.n;
+            pc.h = pw.h;
+            pc.k = pw.k;
+            pc.pad0 = pc.pad1 = 0;
+            pieces[2 * blockIdx.x + slot] = pc;
+          }
+        }
+        tc_fence_before();
+      }
+      down = down_n;
+      qsum = qsum_n;
+      pw = nxt;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (threadIdx.x == 0 && *abort_flag) flag_error(KVQ_DEVERR_TIMEOUT);
+}
+
+// Joins the pieces of the blocks that were cut: a block's pieces are the second
+// place of the CTA where it begins and the first places of the CTAs after it,
+// up to the one marked last. One warp a row, each lane D/32 channels:
+//   m = max m_i, l = sum l_i 2^(m_i - m), out = sum O_i 2^(m_i - m) / l.
+// The order of the pieces is that of the tokens, so the result does not depend
+// on timing.
+template <int D, typename OutT>
+__global__ void __launch_bounds__(256) ragged_merge_kernel(
+    const float* part_o, const float* part_ml, const RgPiece* pieces, int n_ctas, int rows_cap,
+    int pos_per_block, int G, int Hq, OutT* __restrict__ out) {
+  tc::grid_dep_wait();
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  RgPiece pc;
+  {
+    const int4 a = __ldcg(reinterpret_cast<const int4*>(pieces + 2 * c0 + 1));
+    const int4 b = __ldcg(reinterpret_cast<const int4*>(pieces + 2 * c0 + 1) + 1);
+    pc.valid = a.x; pc.last = a.y; pc.row0 = a.z; pc.n = a.w;
+    pc.h = b.x; pc.k = b.y;
+  }
+  if (!pc.valid) return;
+  const int rr = blockIdx.y * 8 + warp;
+  const int j = pc.k * pos_per_block + rr / G;
+  if (rr >= rows_cap || rr >= pos_per_block * G || j >= pc.n) return;
+  // how many pieces follow: the first place marked last, 32 CTAs at a time
+  int n = 0;
+  for (int base = c0 + 1; base < n_ctas; base += 32) {
+    const int c = base + lane;
+    int2 v = make_int2(0, 0);
+    if (c < n_ctas) v = __ldcg(reinterpret_cast<const int2*>(pieces + 2 * c));
+    const unsigned stop = __ballot_sync(0xffffffffu, v.x == 0 || v.y != 0);
+    if (stop) {
+      const int f = __ffs(stop) - 1;
+      n += f + (__shfl_sync(0xffffffffu, v.x, f) ? 1 : 0);
+      break;
+    }
+    n += 32;
+  }
+  const int total = n + 1;
+  auto place = [&](int i) -> int64_t { return (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * rows_cap + rr; };
+  float m = -INFINITY;
+  for (int i = lane; i < total; i += 32) m = fmaxf(m, __ldcg(part_ml + place(i) * 2));
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.f;
+  constexpr int NV = D / 32;
+  float o[NV] = {};
+  float l = 0.f;
+  for (int base = 0; base < total; base += 8) {
+    float2 ml[8];
+    float v[8][NV];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (base + i < total) {
+        const int64_t pl = place(base + i);
+        ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml + pl * 2));
+        if constexpr (NV == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(part_o + pl * D) + lane);
+          v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(part_o + pl * D) + lane);
+          v[i][0] = f.x; v[i][1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (base + i < total) {
+        const float w = exp2f(ml[i].x - m);
+        l += ml[i].y * w;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) o[e] += v[i][e] * w;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  OutT* dst = out + (int64_t(pc.row0 + j) * Hq + pc.h * G + rr % G) * D + lane * NV;
+#pragma unroll
+  for (int e = 0; e < NV; ++e) o[e] *= inv;
+  if constexpr (sizeof(OutT) == 4) {
+    if constexpr (NV == 4) *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    else *reinterpret_cast<float2*>(dst) = make_float2(o[0], o[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < NV; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(o[e], o[e + 1]);
+  }
+}
+
+}  // namespace kvq

@@ -8,6 +8,7 @@ there is no CPU path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -28,6 +29,7 @@ STATIC_FORMATS = ("int8c", "int8t")
 BLOCK_SIZE = 16
 
 DEVERR_SLOT, DEVERR_BLOCK, DEVERR_CONTEXT, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEVERR_RANGE, DEVERR_POSITION = 0x10, 0x20
 
 # Every function the header declares: (name, restype, argtypes)
 _c = ctypes
@@ -70,6 +72,15 @@ _SIGNATURES = [
                                         _c.c_int, _P, _P, _P]),
     ("kvq_prefill_attn_workspace_bytes", _c.c_size_t, [_c.c_int32, _c.c_int32, _c.c_int32,
                                                        _c.c_int32, _c.c_int, _P]),
+    ("kvq_append_rope", _c.c_int, [_P, _c.c_int64, _P, _c.c_int64, _P, _c.c_int64, _P, _P, _c.c_int32,
+                                   _c.c_int32, _c.c_int, _P, _c.c_int32, _P, _P, _P, _P, _P, _c.c_int,
+                                   _P, _P]),
+    ("kvq_read", _c.c_int, [_P, _P, _P, _P, _P, _P, _c.c_int32, _c.c_int32, _P, _P, _c.c_int,
+                            _c.c_int, _P, _P]),
+    ("kvq_ragged_attn_workspace_bytes", _c.c_size_t, [_c.c_int32, _c.c_int, _P]),
+    ("kvq_ragged_attn", _c.c_int, [_P, _c.c_int64, _P, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P,
+                                   _c.c_int32, _c.c_int32, _c.c_float, _P, _c.c_int, _P, _c.c_size_t,
+                                   _c.c_int, _P, _P]),
     ("kvq_prefill_attn", _c.c_int, [_P, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _c.c_int32,
                                     _c.c_float, _P, _c.c_int, _P, _c.c_size_t, _c.c_int32, _c.c_int,
                                     _P, _P]),
@@ -352,6 +363,171 @@ def prefill_attn(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_le
     return out
 
 
+# --------------------------------------------------------------------------- ragged steps
+# These calls launch on the device that holds their tensors, whichever is
+# current, and on its current stream unless one is given. What they allocate
+# themselves (an output or a workspace that is not passed) is allocated on the
+# stream that they launch on.
+def _on(dev, stream):
+    """A context in which `dev` is current and `stream` (or its own current one) too."""
+    if stream is not None and stream.device != dev:
+        raise KvqError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _need_on(dev, t, dtype, name, shape=None):
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise KvqError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise KvqError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _need_cache(dev, k_cache, v_cache, k_scale, v_scale):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise KvqError(f"{name} must be a contiguous tensor on {dev}")
+
+
+def _need_rows(dev, t, name, heads, head_dim):
+    """[T][heads][head_dim] BF16 with the heads of a token contiguous; the
+    stride between tokens in elements."""
+    if t.dtype != torch.bfloat16 or t.device != dev:
+        raise KvqError(f"{name} must be a bfloat16 tensor on {dev}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise KvqError(f"{name} must be [tokens][{heads}][{head_dim}], not {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != head_dim and heads > 1):
+        raise KvqError(f"the values of a token must be contiguous in {name}")
+    return s0 if t.shape[0] > 1 else heads * head_dim
+
+
+def append_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                fmt: str, d: Dims, interleaved=False, stream=None):
+    """Quantize-on-append of keys that the rotary embedding is yet to be applied
+    to (kvq_append_rope). q: [T][Hq][D] bf16 (None: no query), k, v: [T][Hk][D]
+    bf16, all views of one projection's output if that is where they are;
+    positions [T] int32; cos_sin [max_position][rotary_dim] float32 (cosines,
+    then sines); slot_mapping [T] int64 (negative: not stored). q_out [T][Hq][D]
+    receives the rotated query and is returned (None: allocated)."""
+    dev = k.device
+    if not k.is_cuda:
+        raise KvqError("k must be on a CUDA device")
+    T, D = k.shape[0], d.head_dim
+    ks = _need_rows(dev, k, "k", d.n_kv_heads, D)
+    vs = _need_rows(dev, v, "v", d.n_kv_heads, D)
+    if v.shape[0] != T:
+        raise KvqError("k and v must have the same number of tokens")
+    qs = 0
+    if q is not None:
+        qs = _need_rows(dev, q, "q", d.n_q_heads, D)
+        if q.shape[0] != T:
+            raise KvqError("q and k must have the same number of tokens")
+    elif q_out is not None:
+        raise KvqError("q_out without q")
+    _need_on(dev, positions, torch.int32, "positions", (T,))
+    _need_on(dev, slot_mapping, torch.int64, "slot_mapping", (T,))
+    _need_on(dev, cos_sin, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2:
+        raise KvqError("cos_sin must be [max_position][rotary_dim]")
+    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, d.n_q_heads, D), dtype=torch.bfloat16, device=dev)
+        if q_out is not None:
+            _need_on(dev, q_out, torch.bfloat16, "q_out", (T, d.n_q_heads, D))
+        _check(lib().kvq_append_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions),
+                                     _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
+                                     1 if interleaved else 0, _ptr(slot_mapping), T, _ptr(q_out),
+                                     _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     FMT[fmt], ctypes.byref(d), _stream()), "kvq_append_rope")
+    return q_out
+
+
+def read(k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens, total_tokens, fmt: str,
+         d: Dims, k_out=None, v_out=None, out_dtype=torch.bfloat16, stream=None):
+    """Dequantizing read-back (kvq_read): rows cu_tokens[b] .. cu_tokens[b+1]-1 of
+    k_out, v_out [total_tokens][Hk][D] (bf16 or float32) receive the tokens of
+    sequence b from starts[b] on. Outputs not given are allocated; False leaves
+    one out (None is returned in its place)."""
+    dev = block_tables.device
+    if not block_tables.is_cuda:
+        raise KvqError("block_tables must be on a CUDA device")
+    B = starts.numel()
+    _need_on(dev, block_tables, torch.int32, "block_tables", (B, d.max_blocks_per_seq))
+    _need_on(dev, starts, torch.int32, "starts", (B,))
+    _need_on(dev, cu_tokens, torch.int32, "cu_tokens", (B + 1,))
+    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    total = int(total_tokens)
+    shape = (total, d.n_kv_heads, d.head_dim)
+    outs = [k_out, v_out]
+    if outs[0] is False and outs[1] is False:
+        raise KvqError("nothing to read: k_out and v_out are both left out")
+    given = [t for t in outs if isinstance(t, torch.Tensor)]
+    dt = given[0].dtype if given else out_dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise KvqError("outputs must be bfloat16 or float32")
+    if total < 0:
+        raise KvqError("total_tokens must not be negative")
+    with _on(dev, stream):
+        outs = [None if t is False else torch.empty(shape, dtype=dt, device=dev) if t is None else t for t in outs]
+        for t, name in zip(outs, ("k_out", "v_out")):
+            if t is not None:
+                _need_on(dev, t, dt, name, shape)
+        _check(lib().kvq_read(_ptr(k_cache), _ptr(v_cache), _scales(k_scale, v_scale), _ptr(block_tables),
+                              _ptr(starts), _ptr(cu_tokens), B, total, _ptr(outs[0]), _ptr(outs[1]),
+                              0 if dt == torch.bfloat16 else 1, FMT[fmt], ctypes.byref(d), _stream()),
+               "kvq_read")
+    return outs[0], outs[1]
+
+
+def ragged_workspace_bytes(total_q, fmt, d: Dims):
+    """Scratch bytes of kvq_ragged_attn for up to total_q new tokens, on the
+    current device."""
+    n = lib().kvq_ragged_attn_workspace_bytes(int(total_q), FMT[fmt], ctypes.byref(d))
+    if n == 0 and total_q > 0:
+        raise KvqError("kvq_ragged_attn_workspace_bytes: invalid arguments")
+    return n
+
+
+def ragged_attn(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                max_context_len, sm_scale, out, fmt: str, d: Dims, window=0, workspace=None,
+                stream=None):
+    """Attention of ragged chunks of new tokens over the paged cache
+    (kvq_ragged_attn). q: [T][Hq][D] bf16 (a strided view will do), the new tokens
+    of all sequences one after another, cu_q [B + 1] int32 where each begins; they
+    are the last tokens of the sequences' contexts, already appended. out:
+    [T][Hq][D] bf16 or float32."""
+    dev = q.device
+    if not q.is_cuda:
+        raise KvqError("q must be on a CUDA device")
+    T = q.shape[0]
+    qs = _need_rows(dev, q, "q", d.n_q_heads, d.head_dim)
+    B = context_lens.numel()
+    _need_on(dev, cu_q, torch.int32, "cu_q", (B + 1,))
+    _need_on(dev, context_lens, torch.int32, "context_lens", (B,))
+    _need_on(dev, block_tables, torch.int32, "block_tables", (B, d.max_blocks_per_seq))
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise KvqError("out must be bfloat16 or float32")
+    _need_on(dev, out, out.dtype, "out", tuple(q.shape))
+    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    with _on(dev, stream):
+        if workspace is None:
+            workspace = torch.empty(max(ragged_workspace_bytes(T, fmt, d), 16), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise KvqError(f"workspace must be a contiguous tensor on {dev}")
+        _check(lib().kvq_ragged_attn(_ptr(q), qs, _ptr(cu_q), B, T, _ptr(k_cache), _ptr(v_cache),
+                                     _scales(k_scale, v_scale), _ptr(block_tables), _ptr(context_lens),
+                                     int(max_context_len), int(window), float(sm_scale), _ptr(out),
+                                     _out_dtype(out), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), FMT[fmt],
+                                     ctypes.byref(d), _stream()), "kvq_ragged_attn")
+    return out
+
+
 def device_error(clear=True) -> int:
     """KVQ_DEVERR_* bits flagged by kernels on the current device (synchronizes)."""
     f = ctypes.c_uint32()
@@ -443,6 +619,37 @@ class LayerCache:
                             context_lens, max_context_len, sm_scale, out, self.fmt, self.dims,
                             workspace=workspace, partition_tokens=partition_tokens, stream=stream)
 
+    def append_rope(self, q, k, v, positions, cos_sin, slot_mapping, q_out=None, interleaved=False,
+                    stream=None):
+        """Rotate and store new tokens (kvq_append_rope); the rotated query."""
+        return append_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, self.k, self.v,
+                           self.k_scale, self.v_scale, self.fmt, self.dims, interleaved, stream)
+
+    def read(self, block_tables, starts, cu_tokens, total_tokens, k_out=None, v_out=None,
+             out_dtype=torch.bfloat16, stream=None):
+        """Runs of cached tokens as dequantized (K, V) rows (kvq_read)."""
+        return read(self.k, self.v, self.k_scale, self.v_scale, block_tables, starts, cu_tokens,
+                    total_tokens, self.fmt, self.dims, k_out, v_out, out_dtype, stream)
+
+    def ragged_workspace(self, total_q):
+        """Scratch of `ragged` for up to total_q new tokens."""
+        with torch.cuda.device(self.k.device):
+            n = ragged_workspace_bytes(total_q, self.fmt, self.dims)
+            return torch.empty(max(n, 16), dtype=torch.uint8, device=self.k.device)
+
+    def ragged(self, q, cu_q, block_tables, context_lens, max_context_len, sm_scale=None, window=0,
+               out=None, workspace=None, stream=None, out_dtype=torch.bfloat16):
+        """Attention of ragged chunks of new tokens (kvq_ragged_attn): q [T][Hq][D]
+        packed, cu_q [B + 1] where each sequence's rows begin."""
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(self.dims.head_dim)
+        if out is None:
+            with _on(q.device, stream):
+                out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        return ragged_attn(q, cu_q, self.k, self.v, self.k_scale, self.v_scale, block_tables,
+                           context_lens, max_context_len, sm_scale, out, self.fmt, self.dims, window,
+                           workspace, stream)
+
     # ---- copies in the logical layout [NB][Hk][block_size][D] (for inspection and tests)
     def k_logical(self, blocks=None):
         """K of all blocks (or of the block ids `blocks`) as [n][Hk][block_size][D]."""
@@ -495,6 +702,13 @@ class KiviCache:
                                      _ptr(self.k), _ptr(self.v), _ptr(self.k_meta), _ptr(self.v_meta),
                                      FMT[self.fmt], ctypes.byref(self.dims), _stream(stream)),
                "kvq_kivi_append")
+
+    def read(self, block_tables, starts, cu_tokens, total_tokens, k_out=None, v_out=None,
+             out_dtype=torch.bfloat16, stream=None):
+        """Runs of tokens of complete groups as dequantized (K, V) rows (kvq_read);
+        the residual's tokens are read from `residual`."""
+        return read(self.k, self.v, self.k_meta, self.v_meta, block_tables, starts, cu_tokens,
+                    total_tokens, self.fmt, self.dims, k_out, v_out, out_dtype, stream)
 
     def workspace(self, batch, max_quant_len, max_res_len, device="cuda"):
         n = lib().kvq_kivi_decode_workspace_bytes(batch, int(max_quant_len), int(max_res_len),
