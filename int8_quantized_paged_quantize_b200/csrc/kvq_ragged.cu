@@ -46,6 +46,11 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
   auto kern = ragged_mma_kernel<D, FMT, HP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  // the kernel shares its launch's registers out anew; it must own them all
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRgRegs) return cudaErrorInvalidConfiguration;
   const int G = d.n_q_heads / d.n_kv_heads;
   const RgSpace w = rg_space(a.total_q, d);
   char* ws = static_cast<char*>(a.workspace);
@@ -64,7 +69,7 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
   b.window = a.window;
   b.pos_per_block = C::RPB / G;
   const int grid = device_sm_count();                    // one CTA per SM
-  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(448), C::SMEM, st,
+  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kRgThreads), C::SMEM, st,
                  static_cast<const __nv_bfloat16*>(a.q), a.q_stride, static_cast<const uint8_t*>(a.kc),
                  static_cast<const uint8_t*>(a.vc), static_cast<const __nv_bfloat16*>(a.ks),
                  static_cast<const __nv_bfloat16*>(a.vs), a.tables, b, int(d.num_blocks),

@@ -39,13 +39,18 @@
 // finished there; the first and the last of a share may be pieces, whose
 // (m, l, O) go to the workspace (two places a CTA) for ragged_merge_kernel.
 //
-// 14 warps per CTA, one CTA per SM:
+// 16 warps per CTA, one CTA per SM:
 //   0       producer: 1-D bulk copies of 4 K and 4 V pages a step into a ring
 //           of raw stages, the scales beside them by plain loads
-//   1       tensor memory, and one thread that issues the products
-//   2..5    softmax of slot A (thread = row = TMEM lane), 6..9 of slot B
-//   10..13  converters: codes of a step to f16 (BF16 cache: none), V of tokens
+//   1       tensor memory, and one thread that issues the products, whichever
+//           has its operands first
+//   2       walks the CTA's share of the work list and hands the pieces to the
+//           other roles through a ring; 3: none
+//   4..7    softmax of slot A (thread = row = TMEM lane), 8..11 of slot B
+//   12..15  converters: codes of a step to f16 (BF16 cache: none), V of tokens
 //           past the end zeroed, the scales as FP32 column factors
+// The registers are shared out by role: 168 a thread for the softmax warps
+// (64 scores and the weights made of them), 88 for the others.
 //
 // A token whose V row holds a NaN or an infinity (with a per-token scale: whose
 // V scale is one) makes every channel of the rows that attend it NaN and leaves
@@ -53,7 +58,7 @@
 // reach every row, and the rows that attend it get a NaN sum.
 //
 // Every wait is bounded, as in the other attention kernels: on expiry the CTA
-// stops issuing, drains, writes NaN and returns.
+// stops issuing, drains, writes NaN to every row of its share and returns.
 #pragma once
 
 #include "kvq_common.cuh"
@@ -61,6 +66,8 @@
 #include "kvq_ragged_plan.h"
 
 namespace kvq {
+
+constexpr int kRgRing = 4;                     // pieces handed ahead
 
 template <int D, int FMT, bool HP>
 struct RgCfg {
@@ -96,15 +103,23 @@ struct RgCfg {
   static constexpr int OFF_X = OFF_RM + NRAW * RMETA;            // float [16][128]: joining the slots
   static constexpr int OFF_XS = OFF_X + 16 * 128 * 4;            // float4 [128]: m, l, corr of slot B
   static constexpr int OFF_BAR = OFF_XS + 128 * 16;
-  static constexpr int NBAR = 2 * NRAW + 2 * NC + 8 + 2;
+  static constexpr int NBAR = 2 * NRAW + 2 * NC + 8 + 2 + 2 * kRgRing;
   static constexpr int OFF_MASK = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;   // raw page masks [NRAW], then [NC][12]
   static constexpr int OFF_RED = OFF_MASK + 16 * ((NRAW + 3) / 4) + 48 * NC;
   static constexpr int OFF_MISC = OFF_RED + 128;
-  static constexpr int USED = OFF_MISC + 48;
+  static constexpr int OFF_ITEM = OFF_MISC + 48;                 // RgItem [kRgRing]
+  static constexpr int USED = OFF_ITEM + kRgRing * 64;
   // one CTA per SM (it takes all tensor memory): never less than half of an SM's shared memory
-  static constexpr int SMEM = (USED < 118 * 1024 ? 118 * 1024 : USED) + 1024;
+  static constexpr int SMEM = USED < 118 * 1024 ? 118 * 1024 : USED;
   static_assert(OFF_C % 128 == 0 && OFF_Q % 128 == 0 && CSTAGE % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
   static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// A piece as the roles see it: the block's sequence, head and rows, its steps.
+struct __align__(16) RgItem {
+  int b, h, k, rows;                           // rows 0: no more pieces
+  int row0, n, ctx, first;                     // first: token step of the block's step 0
+  int lo, hi, count, pad;
 };
 
 // What describes the batch (device memory) and the shape.
@@ -206,6 +221,18 @@ struct RgPiece {
 };
 static_assert(sizeof(RgPiece) == 32, "layout");
 
+__device__ __forceinline__ void rg_record(RgPiece* p, bool last, int row0, int n, int h, int k) {
+  RgPiece r;
+  r.valid = 1;
+  r.last = last;
+  r.row0 = row0;
+  r.n = n;
+  r.h = h;
+  r.k = k;
+  r.pad0 = r.pad1 = 0;
+  *p = r;
+}
+
 // 1-D bulk copy global -> shared. No L2 hint: the pages of a sequence are read
 // again for its other blocks.
 __device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -229,8 +256,32 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+// Shared memory by its 32-bit address.
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// One arrival for the whole warp, after what its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
+constexpr int kRgThreads = 512;
+constexpr int kRgRegs = 128;                   // registers a thread at launch: 168 + 168 + 88 + 88 = 4 x 128
+
 template <int D, int FMT, bool HP>
-__global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
+__global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     const __nv_bfloat16* __restrict__ q, int64_t q_stride, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const __nv_bfloat16* __restrict__ ks,
     const __nv_bfloat16* __restrict__ vs, const int32_t* __restrict__ tables, const RgBatch bt, int NB,
@@ -238,10 +289,9 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
     float* __restrict__ part_o, float* __restrict__ part_ml, RgPiece* __restrict__ pieces, int rows_cap) {
   using C = RgCfg<D, FMT, HP>;
   using namespace tc;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int NWARPS = 14;
+  constexpr int NWARPS = kRgThreads / 32;
 
   uint8_t* raw = smem + C::OFF_R;
   uint8_t* rmeta = smem + C::OFF_RM;
@@ -258,6 +308,9 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
   uint64_t* pvdone = pready + 2;              // [2] the slot's last PV product has completed
   uint64_t* qready = pvdone + 2;              // the query operand of the next piece
   uint64_t* drain = qready + 1;
+  uint64_t* pfull = drain + 1;                // [kRgRing] a piece is in the ring
+  uint64_t* pfree = pfull + kRgRing;          // [kRgRing] every role has read it
+  RgItem* items = reinterpret_cast<RgItem*>(smem + C::OFF_ITEM);
   volatile uint32_t* rmask = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MASK);
   // per operand stage: {valid pages}, {not-finite V tokens 0..31}, {.. 32..63} as
   // each converter warp saw them
@@ -272,20 +325,24 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NRAW; ++s) {
       mbar_init(rfull + s, 1);
-      mbar_init(rfree + s, C::BF ? 1 : 128);
+      mbar_init(rfree + s, C::BF ? 1 : 4);
     }
     for (int j = 0; j < C::NC; ++j) {
-      mbar_init(cfull + j, 128);
+      mbar_init(cfull + j, 4);
       mbar_init(cfree + j, 1);
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(sfull + j, 1);
-      mbar_init(sfree + j, 128);
-      mbar_init(pready + j, 128);
+      mbar_init(sfree + j, 4);
+      mbar_init(pready + j, 4);
       mbar_init(pvdone + j, 1);
     }
-    mbar_init(qready, 256);
+    mbar_init(qready, 8);
     mbar_init(drain, 1);
+    for (int j = 0; j < kRgRing; ++j) {
+      mbar_init(pfull + j, 1);
+      mbar_init(pfree + j, 14);                // producer, MMA, 8 softmax and 4 converter warps
+    }
     for (int j = 0; j < 3 * C::NC; ++j) cmask[j] = make_uint4(0, 0, 0, 0);
     *abort_flag = 0;
     misci[0] = -1;
@@ -365,95 +422,241 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
       if (misci[0] >= 0) break;                // uniform
     }
   }
-  RgWalk walk;
-  walk.init(bt, misci[0], miscll[0], start, end);
+  // piece i of the share; false when there is none (or the kernel gave up). By
+  // one lane, or by a whole warp (`whole`).
+  auto fetch = [&](int i, RgItem& it, bool whole) -> bool {
+    const int s = i % kRgRing;
+    bool got = mbar_wait(pfull + s, (i / kRgRing) & 1, abort_flag, wait_limit);
+    if (whole) got = __all_sync(0xffffffffu, got);
+    if (!got) return false;
+    const uint32_t a = smem_u32(items + s);
+    const uint4 x = lds_u4(a), y = lds_u4(a + 16), z = lds_u4(a + 32);
+    it.b = int(x.x); it.h = int(x.y); it.k = int(x.z); it.rows = int(x.w);
+    it.row0 = int(y.x); it.n = int(y.y); it.ctx = int(y.z); it.first = int(y.w);
+    it.lo = int(z.x); it.hi = int(z.y); it.count = int(z.z);
+    if (whole) __syncwarp();
+    if (!whole || lane == 0) mbar_arrive(pfree + s);
+    return it.rows > 0;
+  };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
-    const int sp = lane / CPP, sc = lane % CPP;
-    auto step = [&](RgWalk& w, int& i) {
-      if (w.done) return;
-      if (++i >= w.hi) {
-        do w.next(bt); while (!w.done && w.count == 0);
-        i = w.lo;
-      }
-    };
-    // block id of page `lane` of step i (-2: no page there)
-    auto load_id = [&](const RgWalk& w, int i) -> int {
-      if (lane >= C::PPS || w.done) return -2;
-      const int pg = (w.first + i) * C::PPS + lane;
-      return int64_t(pg) * kBlockSize < w.s.ctx ? tables[int64_t(w.b) * bt.W + pg] : -2;
-    };
-    RgWalk c0 = walk;
-    while (!c0.done && c0.count == 0) c0.next(bt);
-    int i0 = c0.lo;
-    RgWalk c1 = c0;
-    int i1 = i0;
-    step(c1, i1);
-    int id0 = load_id(c0, i0);
-    int issued = 0;
-    for (int u = 0; !c0.done; ++u) {
-      const int s = u % C::NRAW;
-      const uint32_t ph = (u / C::NRAW) & 1;
-      const int id1 = load_id(c1, i1);                     // the next step's block ids, in flight
-      const bool valid = id0 >= 0 && id0 < NB;
-      if (id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
-      const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
-      const int64_t page = int64_t(id0) * bt.Hk + c0.h;
-      uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
-      const bool smine = C::MV > 0 && sp < C::PPS && ((mask >> (sp & 3)) & 1u) != 0u;
-      if constexpr (C::MV > 0) {
-        const int sblk = __shfl_sync(0xffffffffu, id0, sp & 3);
-        if (smine) {
-          const int64_t off = (int64_t(sblk) * bt.Hk + c0.h) * C::METAB + sc * 16;
-          kv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ks) + off));
-          vv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(vs) + off));
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
+      const int sp = lane / CPP, sc = lane % CPP;
+      RgItem it;
+      int np = 0, i0 = 0;
+      bool more = true;
+      // the next piece with steps
+      auto next_item = [&]() {
+        do more = fetch(np++, it, true); while (more && it.count == 0);
+        i0 = it.lo;
+      };
+      // block id of page `lane` of step i0 (-2: no page there), and its head
+      int id1 = -2, h1 = 0;
+      auto load_id = [&]() {
+        id1 = -2;
+        h1 = it.h;
+        if (lane >= C::PPS || !more) return;
+        const int pg = (it.first + i0) * C::PPS + lane;
+        if (int64_t(pg) * kBlockSize < it.ctx) id1 = tables[int64_t(it.b) * bt.W + pg];
+      };
+      next_item();
+      load_id();
+      int issued = 0;
+      for (int u = 0, s = 0; more; ++u, s = s + 1 == C::NRAW ? 0 : s + 1) {
+        const uint32_t ph = (u / C::NRAW) & 1;
+        const int id0 = id1, h0 = h1;
+        // the next step's block ids, in flight
+        if (++i0 >= it.hi) next_item();
+        load_id();
+        const bool valid = id0 >= 0 && id0 < NB;
+        if (id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
+        const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
+        const int64_t page = int64_t(id0) * bt.Hk + h0;
+        uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
+        const bool smine = C::MV > 0 && sp < C::PPS && ((mask >> (sp & 3)) & 1u) != 0u;
+        if constexpr (C::MV > 0) {
+          const int sblk = __shfl_sync(0xffffffffu, id0, sp & 3);
+          if (smine) {
+            const int64_t off = (int64_t(sblk) * bt.Hk + h0) * C::METAB + sc * 16;
+            kv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ks) + off));
+            vv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(vs) + off));
+          }
         }
-      }
-      bool ok = true;
-      if (lane == 0) {
-        ok = u < C::NRAW || mbar_wait(rfree + s, ph ^ 1, abort_flag, wait_limit);
-        if (ok) mbar_expect_tx(rfull + s, 2u * uint32_t(__popc(mask)) * uint32_t(C::PAGE));
-      }
-      if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
-      uint8_t* st = raw + s * C::RSTAGE;
-      if (valid) {
-        bulk_g2s_keep(st + lane * C::PAGE, kc + page * C::PAGE, C::PAGE, rfull + s);
-        bulk_g2s_keep(st + (C::PPS + lane) * C::PAGE, vc + page * C::PAGE, C::PAGE, rfull + s);
-      }
-      if constexpr (C::MV > 0) {
-        if (smine) {
-          uint8_t* m = rmeta + s * C::RMETA;
-          *reinterpret_cast<uint4*>(m + sp * C::METAB + sc * 16) = kv;
-          *reinterpret_cast<uint4*>(m + (C::PPS + sp) * C::METAB + sc * 16) = vv;
+        bool ok = true;
+        if (lane == 0) {
+          ok = u < C::NRAW || mbar_wait(rfree + s, ph ^ 1, abort_flag, wait_limit);
+          if (ok) mbar_expect_tx(rfull + s, 2u * uint32_t(__popc(mask)) * uint32_t(C::PAGE));
         }
+        if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
+        uint8_t* st = raw + s * C::RSTAGE;
+        if (valid) {
+          bulk_g2s_keep(st + lane * C::PAGE, kc + page * C::PAGE, C::PAGE, rfull + s);
+          bulk_g2s_keep(st + (C::PPS + lane) * C::PAGE, vc + page * C::PAGE, C::PAGE, rfull + s);
+        }
+        if constexpr (C::MV > 0) {
+          if (smine) {
+            uint8_t* m = rmeta + s * C::RMETA;
+            *reinterpret_cast<uint4*>(m + sp * C::METAB + sc * 16) = kv;
+            *reinterpret_cast<uint4*>(m + (C::PPS + sp) * C::METAB + sc * 16) = vv;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          rmask[s] = mask;
+          mbar_arrive(rfull + s);
+        }
+        issued = u + 1;
       }
-      __syncwarp();
+      if (lane == 0 && *abort_flag) {
+        // the copies already issued land before the CTA's shared memory goes away
+        volatile int no_abort = 0;
+        for (int u = issued > C::NRAW ? issued - C::NRAW : 0; u < issued; ++u)
+          mbar_wait(rfull + u % C::NRAW, (u / C::NRAW) & 1, &no_abort, kMmaWaitLimitCycles);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
       if (lane == 0) {
-        rmask[s] = mask;
-        mbar_arrive(rfull + s);
+        constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
+        constexpr uint32_t id_pv = idesc_f16(D, C::BF);
+        const uint32_t qaddr = smem_u32(qop), raddr = smem_u32(raw), caddr = smem_u32(cst);
+        // Issues whichever product has its operands: the next score product (in the
+        // order of the steps; its K, and S read by the softmax warps), or the PV
+        // product of either slot (its P). `open` counts the products that a stage
+        // still has to feed.
+        RgItem w;
+        int np = 0, i = 0, u = 0, stage = 0, pc = 0, half = 0;
+        bool more = true, want = true;                       // there may be another piece; it is yet to be read
+        uint32_t nqk[2] = {0, 0}, npv[2] = {0, 0};           // score and PV products of each slot so far
+        int step_of[2][2];                                   // stage and whether it opens O, by parity
+        bool opens[2][2];
+        int open[C::NC];
+        bool q_ok = false, k_ok = false;                     // this piece's query, this step's K are there
+        long long idle = clock64();
+        while (more || nqk[0] != npv[0] || nqk[1] != npv[1]) {
+          bool did = false;
+          // never waited for: the softmax warps may have to finish a piece first
+          if (want && mbar_test_wait(pfull + np % kRgRing, (np / kRgRing) & 1)) {
+            more = fetch(np++, w, false);
+            want = more && w.count == 0;
+            i = w.lo;
+            did = true;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (npv[x] == nqk[x] || !mbar_test_wait(pready + x, npv[x] & 1)) continue;
+            tc_fence_after();
+            const int up = (npv[x] & 1) ? step_of[x][1] : step_of[x][0];
+            const bool first = (npv[x] & 1) ? opens[x][1] : opens[x][0];
+            const uint32_t vb = C::BF ? raddr + up * C::RSTAGE + C::PPS * C::PAGE
+                                      : caddr + up * C::CSTAGE + C::PPS * C::CPAGE;
+#pragma unroll
+            for (int j = 0; j < C::PP; ++j)
+#pragma unroll
+              for (int kk = 0; kk < C::PPS; ++kk)
+                mma_f16_ts(tmem + C::COL_O + x * D, tmem + C::COL_P + x * 64 + j * 32 + 8 * kk,
+                           sdesc_plain(vb + kk * C::CPAGE, C::V_LBO, C::V_SBO), id_pv,
+                           (first && j == 0 && kk == 0) ? 0u : 1u);
+            mma_commit(pvdone + x);
+            ++npv[x];
+            did = true;
+            bool last = false;
+#pragma unroll
+            for (int j = 0; j < C::NC; ++j)
+              if (j == up) last = --open[j] == 0;
+            if (last) mma_commit(C::BF ? rfree + up : cfree + up);   // the stage is free
+          }
+          if (more && !want) {
+            const bool two = w.rows > 128;
+            const int x = two ? half : (i - w.lo) & 1;
+            if (!q_ok) q_ok = mbar_test_wait(qready, pc & 1);
+            if (q_ok && !k_ok) k_ok = mbar_test_wait(cfull + stage, (u / C::NC) & 1);
+            const uint32_t n = x ? nqk[1] : nqk[0], v = x ? npv[1] : npv[0];
+            // S of the slot's last product has been read; at most one P is due
+            if (k_ok && n - v < 2 && (n == 0 || mbar_test_wait(sfree + x, (n - 1) & 1))) {
+              tc_fence_after();
+              const uint32_t kb = C::BF ? raddr + stage * C::RSTAGE : caddr + stage * C::CSTAGE;
+              const uint32_t qa = qaddr + (two ? x : 0) * C::QBYTES;
+#pragma unroll
+              for (int qp = 0; qp < C::QP; ++qp)
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                  mma_ss<0>(tmem + C::COL_S + x * 64,
+                            sdesc_plain(qa + qp * C::QBYTES + kk * 256, C::Q_LBO, C::Q_SBO),
+                            sdesc_plain(kb + kk * 256, C::K_LBO, C::K_SBO), id_s, (qp | kk) ? 1u : 0u);
+              mma_commit(sfull + x);
+              const bool opening = two ? i == w.lo : i - w.lo < 2;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (y == x) {
+                  if (nqk[y] & 1) { step_of[y][1] = stage; opens[y][1] = opening; }
+                  else { step_of[y][0] = stage; opens[y][0] = opening; }
+                  ++nqk[y];
+                }
+              if (half == 0) {
+#pragma unroll
+                for (int j = 0; j < C::NC; ++j)
+                  if (j == stage) open[j] = two ? 2 : 1;
+              }
+              did = true;
+              if (two && half == 0) {
+                half = 1;
+              } else {
+                half = 0;
+                k_ok = false;
+                ++u;
+                stage = stage + 1 == C::NC ? 0 : stage + 1;
+                if (++i >= w.hi) {
+                  want = true;
+                  ++pc;
+                  q_ok = false;
+                }
+              }
+            }
+          }
+          if (did) {
+            idle = clock64();
+          } else {
+            if (*abort_flag) break;
+            if (clock64() - idle > wait_limit) {
+              *abort_flag = 1;
+              break;
+            }
+          }
+        }
+        // every product issued completes before tensor memory is released
+        volatile int no_abort = 0;
+        mma_commit(drain);
+        mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
       }
-      issued = u + 1;
-      c0 = c1;
-      i0 = i1;
-      id0 = id1;
-      step(c1, i1);
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- the pieces
+      RgWalk w;
+      w.init(bt, misci[0], miscll[0], start, end);
+      for (int i = 0;; ++i) {
+        const int s = i % kRgRing;
+        if (i >= kRgRing && !mbar_wait(pfree + s, (i / kRgRing - 1) & 1, abort_flag, wait_limit)) break;
+        RgItem it;
+        it.b = w.b; it.h = w.h; it.k = w.k; it.rows = w.done ? 0 : w.rows;
+        it.row0 = w.row0; it.n = w.s.n; it.ctx = w.s.ctx; it.first = w.first;
+        it.lo = w.lo; it.hi = w.hi; it.count = w.count; it.pad = 0;
+        items[s] = it;
+        mbar_arrive(pfull + s);
+        if (w.done) break;
+        w.next(bt);
+      }
     }
-    if (lane == 0 && *abort_flag) {
-      // the copies already issued land before the CTA's shared memory goes away
-      volatile int no_abort = 0;
-      for (int u = issued > C::NRAW ? issued - C::NRAW : 0; u < issued; ++u)
-        mbar_wait(rfull + u % C::NRAW, (u / C::NRAW) & 1, &no_abort, kMmaWaitLimitCycles);
-    }
-  } else if (warp >= 10) {
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ---------------------------------------------------------- converters
-    const int ct = threadIdx.x - 320;                      // 0 .. 127
+    const int ct = threadIdx.x - 384;                      // 0 .. 127
     bool ok = true;
-    int u = 0;
-    for (RgWalk w = walk; !w.done; w.next(bt)) {
-      for (int i = w.lo; i < w.hi; ++i, ++u) {
-        const int s = u % C::NRAW, cs = u % C::NC;
+    int u = 0, s = 0, cs = 0;                              // step, its raw and operand stage
+    RgItem w;
+    for (int np = 0; ok && fetch(np, w, true); ++np) {
+      for (int i = w.lo; ok && i < w.hi; ++i, ++u, s = s + 1 == C::NRAW ? 0 : s + 1, cs = cs + 1 == C::NC ? 0 : cs + 1) {
         if (ok) ok = mbar_wait(rfull + s, (u / C::NRAW) & 1, abort_flag, wait_limit);
         if (ok && !C::BF && u >= C::NC) ok = mbar_wait(cfree + cs, (u / C::NC - 1) & 1, abort_flag, wait_limit);
         ok = __all_sync(0xffffffffu, ok);                  // what follows votes and reduces over the warp
@@ -466,7 +669,7 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
         // tokens of page p that hold cache entries
         auto nvalid = [&](int p) -> int {
           if (((pm >> p) & 1u) == 0u) return 0;
-          return max(0, min(16, w.s.ctx - (tok0 + 16 * p)));
+          return max(0, min(16, w.ctx - (tok0 + 16 * p)));
         };
         if (ok) {
           if constexpr (C::BF) {
@@ -513,8 +716,8 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
               cmw[8 + (ct >> 5)] = bad1;
             }
           } else {
-            uint8_t* ck = cb;
-            uint8_t* cv = cb + C::PPS * C::CPAGE;
+            const uint32_t rka = smem_u32(rk), rva = smem_u32(rv);
+            const uint32_t cka = smem_u32(cb), cva = cka + C::PPS * C::CPAGE;
             float* cm = reinterpret_cast<float*>(cb + 2 * C::PPS * C::CPAGE);
             const uint8_t* mk = rmeta + s * C::RMETA;
             const uint8_t* mv = mk + C::PPS * C::METAB;
@@ -524,8 +727,8 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
 #pragma unroll
             for (int it = 0; it < NIT; ++it) {
               const int x = ct + 128 * it;                 // K: 16 channels of a token; V: 16 tokens of a channel
-              kraw[it] = *reinterpret_cast<const uint4*>(rk + x * 16);
-              vraw[it] = *reinterpret_cast<const uint4*>(rv + x * 16);
+              kraw[it] = lds_u4(rka + x * 16);
+              vraw[it] = lds_u4(rva + x * 16);
             }
             // per-token column factors: score = S a + b qsum, weight P sv, V zero point zv
             if (ct < C::ST) {
@@ -569,9 +772,9 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
               const int g = k / (D / 2), rem = k % (D / 2), c = rem >> 3, tt = rem & 7;
               uint4 o0, o1;
               codes16_to_f16<FMT>(kraw[it], o0, o1);
-              uint8_t* dst = ck + p * C::CPAGE + g * 16 * D + (2 * c) * 128 + tt * 16;
-              *reinterpret_cast<uint4*>(dst) = o0;
-              *reinterpret_cast<uint4*>(dst + 128) = o1;
+              const uint32_t dst = cka + p * C::CPAGE + g * 16 * D + (2 * c) * 128 + tt * 16;
+              sts_u4(dst, o0.x, o0.y, o0.z, o0.w);
+              sts_u4(dst + 128, o1.x, o1.y, o1.z, o1.w);
             }
 #pragma unroll
             for (int it = 0; it < NIT; ++it) {
@@ -591,102 +794,24 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
                 for (int e = 0; e < 8; ++e)
                   wv[e] &= ((keep >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((keep >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
               }
-              uint8_t* pg = cv + p * C::CPAGE;
-              *reinterpret_cast<uint4*>(pg + d * 16) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-              *reinterpret_cast<uint4*>(pg + (D + d) * 16) = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+              const uint32_t pg = cva + p * C::CPAGE;
+              sts_u4(pg + d * 16, wv[0], wv[1], wv[2], wv[3]);
+              sts_u4(pg + (D + d) * 16, wv[4], wv[5], wv[6], wv[7]);
             }
           }
           fence_proxy_async_smem();
         }
-        mbar_arrive(cfull + cs);
-        if constexpr (!C::BF) mbar_arrive(rfree + s);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
-      constexpr uint32_t id_pv = idesc_f16(D, C::BF);
-      const uint32_t qaddr = smem_u32(qop), raddr = smem_u32(raw), caddr = smem_u32(cst);
-      bool ok = true;
-      int u = 0, pc = 0;
-      uint32_t cnt[2] = {0, 0};                            // steps of each slot so far
-      // a slot's PV product that waits for its P
-      int pend[2] = {-1, -1};                              // its step
-      bool pend_first[2] = {false, false}, pend_free[2] = {false, false};
-      auto issue_pv = [&](int x) -> bool {
-        if (pend[x] < 0) return true;
-        if (!mbar_wait(pready + x, (cnt[x] - 1) & 1, abort_flag, wait_limit)) return false;
-        tc_fence_after();
-        const int up = pend[x];
-        const uint32_t vb = C::BF ? raddr + (up % C::NRAW) * C::RSTAGE + C::PPS * C::PAGE
-                                  : caddr + (up % C::NC) * C::CSTAGE + C::PPS * C::CPAGE;
-#pragma unroll
-        for (int j = 0; j < C::PP; ++j)
-#pragma unroll
-          for (int kk = 0; kk < C::PPS; ++kk)
-            mma_f16_ts(tmem + C::COL_O + x * D, tmem + C::COL_P + x * 64 + j * 32 + 8 * kk,
-                       sdesc_plain(vb + kk * C::CPAGE, C::V_LBO, C::V_SBO), id_pv,
-                       (pend_first[x] && j == 0 && kk == 0) ? 0u : 1u);
-        mma_commit(pvdone + x);
-        if (pend_free[x]) {
-          // the step's last product: its stage is free
-          if constexpr (C::BF) mma_commit(rfree + up % C::NRAW);
-          else mma_commit(cfree + up % C::NC);
-        }
-        pend[x] = -1;
-        return true;
-      };
-      auto issue_qk = [&](int x, int step, bool first, bool frees, int qx) -> bool {
-        if (cnt[x] > 0 && !mbar_wait(sfree + x, (cnt[x] - 1) & 1, abort_flag, wait_limit)) return false;
-        tc_fence_after();
-        const uint32_t kb = C::BF ? raddr + (step % C::NRAW) * C::RSTAGE : caddr + (step % C::NC) * C::CSTAGE;
-#pragma unroll
-        for (int qp = 0; qp < C::QP; ++qp)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss<0>(tmem + C::COL_S + x * 64,
-                      sdesc_plain(qaddr + (qp + qx) * C::QBYTES + kk * 256, C::Q_LBO, C::Q_SBO),
-                      sdesc_plain(kb + kk * 256, C::K_LBO, C::K_SBO), id_s, (qp | kk) ? 1u : 0u);
-        mma_commit(sfull + x);
-        // the PV product of the slot's step before
-        if (!issue_pv(x)) return false;
-        pend[x] = step;
-        pend_first[x] = first;
-        pend_free[x] = frees;
-        ++cnt[x];
-        return true;
-      };
-      for (RgWalk w = walk; ok && !w.done; w.next(bt)) {
-        if (w.count == 0) continue;
-        const bool two = w.rows > 128;
-        ok = mbar_wait(qready, pc & 1, abort_flag, wait_limit);
-        ++pc;
-        for (int i = w.lo; ok && i < w.hi; ++i, ++u) {
-          ok = mbar_wait(cfull + u % C::NC, (u / C::NC) & 1, abort_flag, wait_limit);
-          if (!ok) break;
-          if (two) {
-            ok = issue_qk(0, u, i == w.lo, false, 0) && issue_qk(1, u, i == w.lo, true, 1);
-          } else {
-            const int x = (i - w.lo) & 1;
-            ok = issue_qk(x, u, i - w.lo < 2, true, 0);
-          }
-        }
-        // in the order of the steps, so that stages come free in order
-        if (ok) {
-          const int a = pend[1] >= 0 && (pend[0] < 0 || pend[1] < pend[0]) ? 1 : 0;
-          ok = issue_pv(a) && issue_pv(a ^ 1);
+        warp_arrive(cfull + cs, lane);
+        if constexpr (!C::BF) {
+          if (lane == 0) mbar_arrive(rfree + s);
         }
       }
-      // every product issued completes before tensor memory is released
-      volatile int no_abort = 0;
-      mma_commit(drain);
-      mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ---------------------------------------------------------- softmax warps
     const int quarter = warp & 3;
-    const int x = (warp - 2) >> 2;                         // slot
+    const int x = (warp - 4) >> 2;                         // slot
     const int r = quarter * 32 + lane;                     // row of the slot, TMEM lane
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     const uint32_t t_o = tmem + lane_base + C::COL_O + x * D;
@@ -702,15 +827,15 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
       ok = __all_sync(0xffffffffu, ok);
     };
     // this thread's row of a block: the block row, its token of the sequence's new ones
-    auto block_row = [&](const RgWalk& w) -> int { return w.rows > 128 ? x * 128 + r : r; };
-    auto token_of = [&](const RgWalk& w, int rr) -> int { return w.k * bt.pos_per_block + (rr >> gshift); };
-    auto head_of = [&](const RgWalk& w, int rr) -> int { return (w.h << gshift) + (rr & (bt.G - 1)); };
+    auto block_row = [&](const RgItem& w) -> int { return w.rows > 128 ? x * 128 + r : r; };
+    auto token_of = [&](const RgItem& w, int rr) -> int { return w.k * bt.pos_per_block + (rr >> gshift); };
+    auto head_of = [&](const RgItem& w, int rr) -> int { return (w.h << gshift) + (rr & (bt.G - 1)); };
 
     // The query row of a piece into the operand (K-major 8-row groups of
     // 16-byte chunks). `down` takes S back to the row's units, qsum is the sum of
     // the operand's values (the zero-point term). With one block of rows for
     // both slots, slot A's warps write it.
-    auto store_q = [&](const RgWalk& w, float& down, float& qsum) {
+    auto store_q = [&](const RgItem& w, float& down, float& qsum) {
       down = 1.f;
       qsum = 0.f;
       const bool two = w.rows > 128;
@@ -803,35 +928,47 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
         reinterpret_cast<uint4*>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
       }
     };
-    // blocks in which no row attends anything: zero rows
-    auto skip_empty = [&](RgWalk& w) {
-      while (!w.done && w.count == 0) {
+    // The next piece with steps; blocks in which no row attends anything get
+    // their zero rows here. The two warps of a lane quarter meet at barriers, so
+    // they go on together or not at all.
+    int np = 0;
+    auto next_item = [&](RgItem& w) -> bool {
+      while (true) {
+        const bool mine = ok && fetch(np++, w, true);
+        uint32_t both;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+            "barrier.cta.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+            : "=r"(both)
+            : "r"(uint32_t(mine)), "r"(pair_bar)
+            : "memory");
+        if (both == 0u) return false;
+        if (w.count > 0) return true;
         const int rr = block_row(w);
         if (rr < w.rows && (w.rows > 128 || x == 0)) {
           OutT* dst = out + (int64_t(w.row0 + token_of(w, rr)) * (bt.Hk << gshift) + head_of(w, rr)) * D;
           const float z[16] = {};
           for (int c = 0; c < D / 16; ++c) store_row16(dst + 16 * c, z);
         }
-        w.next(bt);
       }
     };
 
-    RgWalk pw = walk;
-    skip_empty(pw);
+    RgItem pw;
+    bool more = next_item(pw);
     float down = 1.f, qsum = 0.f;
-    if (!pw.done) {
+    if (more) {
       store_q(pw, down, qsum);
-      mbar_arrive(qready);
+      warp_arrive(qready, lane);
     }
     int u0 = 0;                                            // the piece's first step
     uint32_t cnt = 0, cnt_other = 0;                       // steps of this slot and of the other so far
-    while (!pw.done) {
+    while (more) {
       const bool two = pw.rows > 128;
       const int rr = block_row(pw);
       const bool row_ok = rr < pw.rows;
       const bool active = __any_sync(0xffffffffu, row_ok);
       const int nsteps = pw.hi - pw.lo;
-      const int p = pw.s.ctx - pw.s.n + token_of(pw, rr);
+      const int p = pw.ctx - pw.n + token_of(pw, rr);
       // tokens lo_t <= t < lim are attended; rows past the block's see everything
       // (nothing of them is written)
       const int lim = row_ok ? max(0, p + 1) : INT_MAX;
@@ -840,28 +977,26 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
       bool any_step = false;
       for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
         const int u = u0 + i, ck = u % C::NC;
-        wait_all(cfull + ck, (u / C::NC) & 1);
-        wait_all(sfull + x, cnt & 1);
+        // both at once: they are mostly complete
+        if (!__all_sync(0xffffffffu, mbar_test_wait(sfull + x, cnt & 1) & mbar_test_wait(cfull + ck, (u / C::NC) & 1))) {
+          wait_all(sfull + x, cnt & 1);
+          wait_all(cfull + ck, (u / C::NC) & 1);
+        }
         tc_fence_after();
         if (!active) {
-          mbar_arrive(sfree + x);
+          warp_arrive(sfree + x, lane);
           if (cnt > 0) wait_all(pvdone + x, (cnt - 1) & 1);
-          mbar_arrive(pready + x);
+          warp_arrive(pready + x, lane);
           ++cnt;
           continue;
         }
         uint32_t sr[C::ST];
-        if (ok) {
-          tmem_ld32(t_s, sr);
-          tmem_ld32(t_s + 32, sr + 32);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int c = 0; c < C::ST; ++c) sr[c] = 0u;
-        }
+        tmem_ld32(t_s, sr);
+        tmem_ld32(t_s + 32, sr + 32);
+        tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(sfree + x);
-        const float* cm = reinterpret_cast<const float*>(cst + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
+        warp_arrive(sfree + x, lane);
+        const uint32_t cma = smem_u32(cst) + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE);
         const uint32_t pages_ok = cmask[3 * ck].x;
         const uint4 wl = cmask[3 * ck + 1], wh = cmask[3 * ck + 2];
         const uint32_t wild0 = wl.x | wl.y | wl.z | wl.w, wild1 = wh.x | wh.y | wh.z | wh.w;
@@ -870,15 +1005,25 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
                                                       (wild0 | wild1) == 0u);
         // scores in the operand's units (times `down`: base-2 scores), in place of S
         float2* x2 = reinterpret_cast<float2*>(sr);
-        const float2* a2 = reinterpret_cast<const float2*>(cm);
-        const float2* b2 = reinterpret_cast<const float2*>(cm + C::ST);
         const float2 qs2 = make_float2(qsum, qsum), k2 = make_float2(qk_scale, qk_scale);
 #pragma unroll
-        for (int k = 0; k < C::ST / 2; ++k) {
-          const float2 sv_ = make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
-          if constexpr (C::BF || C::SI) x2[k] = __fmul2_rn(sv_, k2);
-          else if constexpr (C::ZP) x2[k] = __ffma2_rn(sv_, a2[k], __fmul2_rn(b2[k], qs2));
-          else x2[k] = __fmul2_rn(sv_, a2[k]);
+        for (int k = 0; k < C::ST / 2; k += 2) {
+          const float2 s0 = make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
+          const float2 s1 = make_float2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3]));
+          if constexpr (C::BF || C::SI) {
+            x2[k] = __fmul2_rn(s0, k2);
+            x2[k + 1] = __fmul2_rn(s1, k2);
+          } else {
+            const float4 a = lds_f4(cma + 8 * k);
+            if constexpr (C::ZP) {
+              const float4 b = lds_f4(cma + 4 * C::ST + 8 * k);
+              x2[k] = __ffma2_rn(s0, make_float2(a.x, a.y), __fmul2_rn(make_float2(b.x, b.y), qs2));
+              x2[k + 1] = __ffma2_rn(s1, make_float2(a.z, a.w), __fmul2_rn(make_float2(b.z, b.w), qs2));
+            } else {
+              x2[k] = __fmul2_rn(s0, make_float2(a.x, a.y));
+              x2[k + 1] = __fmul2_rn(s1, make_float2(a.z, a.w));
+            }
+          }
         }
         bool wild = false;
         if (!full) {
@@ -896,62 +1041,63 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
             if (!((v1 >> c) & 1u)) sr[32 + c] = 0xff800000u;
           }
         }
-        float mt = -INFINITY;
+        float mt;
         {
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+          float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < C::ST; k += 4) {
-            m0 = fmaxf(m0, __uint_as_float(sr[k]));
-            m1 = fmaxf(m1, __uint_as_float(sr[k + 1]));
-            m2 = fmaxf(m2, __uint_as_float(sr[k + 2]));
-            m3 = fmaxf(m3, __uint_as_float(sr[k + 3]));
+            m0 = max3(m0, __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
+            m1 = max3(m1, __uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3]));
           }
-          mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * down;
+          mt = fmaxf(m0, m1) * down;
         }
-        if constexpr (C::F8 || C::ZP) mt += fmaxf(cm[4 * C::ST], cm[4 * C::ST + 1]);
-        float alpha = 1.f;
-        if (mt > m_run + 8.f) {
-          if (m_run != -INFINITY) {
-            alpha = exp2f(m_run - mt);
-            l *= alpha;
-            corr *= alpha;
-          }
-          m_run = mt;
+        if constexpr (C::F8 || C::ZP) {
+          const float4 lt = lds_f4(cma + 16 * C::ST);      // log2 of the largest V scales
+          mt += fmaxf(lt.x, lt.y);
         }
+        const bool move = mt > m_run + 8.f;
+        const float alpha = move && m_run != -INFINITY ? ex2_ftz(m_run - mt) : 1.f;
+        m_run = move ? mt : m_run;
+        l *= alpha;
+        corr *= alpha;
         const float mref = m_run == -INFINITY ? 0.f : m_run;
         const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
         if (rescale) {
           wait_all(pvdone + x, (cnt - 1) & 1);
           tc_fence_after();
-          if (ok) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t ov[16];
-              tmem_ld16(t_o + 16 * c, ov);
-              tmem_ld_wait();
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16(t_o + 16 * c, ov);
+            tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-              tmem_st16(t_o + 16 * c, ov);
-            }
-            tmem_st_wait();
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st16(t_o + 16 * c, ov);
           }
+          tmem_st_wait();
         }
         // weights, 32 tokens at a time, as pairs of 16-bit values
         const float2 dn2 = make_float2(down, down), nm2 = make_float2(-mref, -mref);
-        const float2* sv2 = reinterpret_cast<const float2*>(cm + 2 * C::ST);
-        const float2* zv2 = reinterpret_cast<const float2*>(cm + 3 * C::ST);
         float2 ls2 = make_float2(0.f, 0.f), cz2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
+          float4 sv4 = make_float4(1.f, 1.f, 1.f, 1.f), zv4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int kk = 16 * hf + k;
+            if constexpr (C::F8 || C::ZP) {
+              if ((k & 1) == 0) sv4 = lds_f4(cma + 8 * C::ST + 8 * kk);
+            }
+            if constexpr (C::ZP) {
+              if ((k & 1) == 0) zv4 = lds_f4(cma + 12 * C::ST + 8 * kk);
+            }
             const float2 e = __ffma2_rn(x2[kk], dn2, nm2);
             const float2 p2 = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
             ls2 = __fadd2_rn(ls2, p2);
             float2 wv = p2;
-            if constexpr (C::F8 || C::ZP) wv = __fmul2_rn(p2, sv2[kk]);
+            if constexpr (C::F8 || C::ZP)
+              wv = __fmul2_rn(p2, (k & 1) ? make_float2(sv4.z, sv4.w) : make_float2(sv4.x, sv4.y));
             float2 hv;
             if constexpr (C::BF) {
               const __nv_bfloat162 b16 = __floats2bfloat162_rn(wv.x, wv.y);
@@ -973,24 +1119,23 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
                 if constexpr (C::ZP) hv = __fadd2_rn(hv, __half22float2(f16));
               }
             }
-            if constexpr (C::ZP) cz2 = __ffma2_rn(hv, zv2[kk], cz2);
+            if constexpr (C::ZP)
+              cz2 = __ffma2_rn(hv, (k & 1) ? make_float2(zv4.z, zv4.w) : make_float2(zv4.x, zv4.y), cz2);
           }
           // the last product has read P
           if (hf == 0 && cnt > 0 && !rescale) {
             wait_all(pvdone + x, (cnt - 1) & 1);
             tc_fence_after();
           }
-          if (ok) {
-            tmem_st16(t_p + 16 * hf, ph);
-            if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 16 * hf, pl);
-          }
+          tmem_st16(t_p + 16 * hf, ph);
+          if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 16 * hf, pl);
         }
         l += ls2.x + ls2.y;
         corr += cz2.x + cz2.y;
         if (wild) l = __int_as_float(0x7fc00000);
-        if (ok) tmem_st_wait();
+        tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(pready + x);
+        warp_arrive(pready + x, lane);
         ++cnt;
         any_step = true;
       }
@@ -999,55 +1144,47 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
       u0 += nsteps;
 
       // the next piece's query, once the products that read this one's have completed
-      RgWalk nxt = pw;
-      nxt.next(bt);
-      skip_empty(nxt);
+      RgItem nxt;
+      const bool more_n = next_item(nxt);
       float down_n = 1.f, qsum_n = 0.f;
-      if (!nxt.done) {
+      if (more_n) {
         if (!two && x == 0 && nsteps > 1) wait_all(sfull + 1, (cnt_other - 1) & 1);
         store_q(nxt, down_n, qsum_n);
-        mbar_arrive(qready);
+        warp_arrive(qready, lane);
       }
 
       // ---- the piece's end: O of the last step
       if (any_step) wait_all(pvdone + x, (cnt - 1) & 1);
       tc_fence_after();
-      bool good = __all_sync(0xffffffffu, ok && !*abort_flag);
       float ma = 1.f, mb = 0.f;                            // O = ma O_A + mb O_B (one block of rows)
       if (!two && active) {
-        if (x == 1) {
-          xsum[r] = make_float4(any_step ? m_run : -INFINITY, any_step ? l : 0.f, any_step ? corr : 0.f, good ? 1.f : 0.f);
-        }
+        if (x == 1) xsum[r] = any_step ? make_float4(m_run, l, corr, 0.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         named_bar_sync(pair_bar, 64);
         if (x == 0) {
           const float4 o = xsum[r];
-          good = __all_sync(0xffffffffu, good && o.w != 0.f);
           const float m = fmaxf(m_run, o.x);
           const float mr = m == -INFINITY ? 0.f : m;
-          ma = exp2f(m_run - mr);
-          mb = exp2f(o.x - mr);
+          ma = ex2_ftz(m_run - mr);
+          mb = ex2_ftz(o.x - mr);
           l = l * ma + o.y * mb;
           corr = corr * ma + o.z * mb;
           m_run = m;
         }
       }
       if (active) {
-        const bool whole = pw.whole();
+        const bool whole = pw.lo == 0 && pw.hi == pw.count;
         const int slot = pw.lo == 0 ? 1 : 0;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         const int64_t orow = int64_t(pw.row0 + (row_ok ? token_of(pw, rr) : 0)) * (bt.Hk << gshift) + head_of(pw, rr);
         const int64_t prow = (int64_t(blockIdx.x) * 2 + slot) * rows_cap + rr;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t ov[16];
-          const bool have = good && any_step;
-          if (have) {
-            tmem_ld16(t_o + 16 * c, ov);
-            tmem_ld_wait();
-          }
+          tmem_ld16(t_o + 16 * c, ov);
+          tmem_ld_wait();
           float o[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = have ? __uint_as_float(ov[e]) : 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = any_step ? __uint_as_float(ov[e]) : 0.f;
           if (!two) {
             if (x == 1) {
 #pragma unroll
@@ -1065,8 +1202,7 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
             for (int e = 0; e < 16; ++e) {
               float y = o[e] - corr;
               if constexpr (C::SI) y *= __bfloat162float(vs[per_tensor ? 0 : pw.h * D + 16 * c + e]);
-              if (whole) y *= inv;
-              o[e] = good ? y : __int_as_float(0x7fc00000);
+              o[e] = y * inv;
             }
             if (whole) {
               store_row16(out + orow * D + 16 * c, o);
@@ -1079,26 +1215,15 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
           }
         }
         if (!whole && (two || x == 0)) {
-          if (row_ok)
-            *reinterpret_cast<float2*>(part_ml + prow * 2) =
-                good ? make_float2(m_run, l) : make_float2(INFINITY, __int_as_float(0x7fc00000));
-          if (x == 0 && r == 0) {
-            RgPiece pc;
-            pc.valid = 1;
-            pc.last = pw.hi == pw.count;
-            pc.row0 = pw.row0;
-            pc.n = pw.s.n;
-            pc.h = pw.h;
-            pc.k = pw.k;
-            pc.pad0 = pc.pad1 = 0;
-            pieces[2 * blockIdx.x + slot] = pc;
-          }
+          if (row_ok) *reinterpret_cast<float2*>(part_ml + prow * 2) = make_float2(m_run, l);
+          if (x == 0 && r == 0) rg_record(pieces + 2 * blockIdx.x + slot, pw.hi == pw.count, pw.row0, pw.n, pw.h, pw.k);
         }
         tc_fence_before();
       }
       down = down_n;
       qsum = qsum_n;
       pw = nxt;
+      more = more_n;
     }
   }
   tc_fence_before();
@@ -1107,7 +1232,29 @@ __global__ void __launch_bounds__(448, 1) ragged_mma_kernel(
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (threadIdx.x == 0 && *abort_flag) flag_error(KVQ_DEVERR_TIMEOUT);
+  if (*abort_flag) {
+    // what this CTA was to write becomes NaN
+    if (threadIdx.x == 0) flag_error(KVQ_DEVERR_TIMEOUT);
+    using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
+    OutT* out = static_cast<OutT*>(out_);
+    const float nan = __int_as_float(0x7fc00000);
+    RgWalk w;
+    for (w.init(bt, misci[0], miscll[0], start, end); !w.done; w.next(bt)) {
+      const int slot = w.lo == 0 ? 1 : 0;
+      for (int j = threadIdx.x; j < w.rows * D; j += blockDim.x) {
+        const int rr = j / D, d = j % D;
+        if (w.whole()) {
+          const int64_t row = int64_t(w.row0 + w.k * bt.pos_per_block + rr / bt.G) * (bt.Hk * bt.G) + w.h * bt.G + rr % bt.G;
+          if constexpr (HP) out[row * D + d] = nan;
+          else out[row * D + d] = __float2bfloat16_rn(nan);
+        } else if (d < 2) {
+          part_ml[((int64_t(blockIdx.x) * 2 + slot) * rows_cap + rr) * 2 + d] = d ? nan : INFINITY;
+        }
+      }
+      if (!w.whole() && threadIdx.x == 0)
+        rg_record(pieces + 2 * blockIdx.x + slot, w.hi == w.count, w.row0, w.s.n, w.h, w.k);
+    }
+  }
 }
 
 // Joins the pieces of the blocks that were cut: a block's pieces are the second
