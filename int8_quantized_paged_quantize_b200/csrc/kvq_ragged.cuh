@@ -42,8 +42,7 @@
 // 16 warps per CTA, one CTA per SM:
 //   0       producer: 1-D bulk copies of 4 K and 4 V pages a step into a ring
 //           of raw stages, the scales beside them by plain loads
-//   1       tensor memory, and one thread that issues the products, whichever
-//           has its operands first
+//   1       tensor memory, and one thread that issues the products
 //   2       walks the CTA's share of the work list and hands the pieces to the
 //           other roles through a ring; 3: none
 //   4..7    softmax of slot A (thread = row = TMEM lane), 8..11 of slot B
@@ -257,11 +256,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 }
 
 // Shared memory by its 32-bit address.
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -275,6 +269,39 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) tc::mbar_arrive(bar);
+}
+
+// A product must cost the thread that issues it few instructions (the 64-bit
+// descriptors built anew for each took it a thousand cycles a step). The
+// high words of the shared-memory descriptors (stride, version; see sdesc_plain) are
+// constants, the low words (address / 16, leading offset) advance by additions.
+template <uint32_t SBO>
+__host__ __device__ constexpr uint32_t rg_desc_hi() { return (SBO >> 4) | (1u << 14); }
+template <uint32_t LBO>
+__device__ __forceinline__ uint32_t rg_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((LBO >> 4) << 16); }
+template <uint32_t AHI, uint32_t BHI>
+__device__ __forceinline__ void rg_mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "n"(AHI), "n"(BHI)
+      : "memory");
+}
+template <uint32_t BHI>
+__device__ __forceinline__ void rg_mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(blo), "r"(idesc), "r"(acc), "n"(BHI)
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+  return e != 0u;
 }
 
 constexpr int kRgThreads = 512;
@@ -518,119 +545,104 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
-        constexpr uint32_t id_pv = idesc_f16(D, C::BF);
-        const uint32_t qaddr = smem_u32(qop), raddr = smem_u32(raw), caddr = smem_u32(cst);
-        // Issues whichever product has its operands: the next score product (in the
-        // order of the steps; its K, and S read by the softmax warps), or the PV
-        // product of either slot (its P). `open` counts the products that a stage
-        // still has to feed.
-        RgItem w;
-        int np = 0, i = 0, u = 0, stage = 0, pc = 0, half = 0;
-        bool more = true, want = true;                       // there may be another piece; it is yet to be read
-        uint32_t nqk[2] = {0, 0}, npv[2] = {0, 0};           // score and PV products of each slot so far
-        int step_of[2][2];                                   // stage and whether it opens O, by parity
-        bool opens[2][2];
-        int open[C::NC];
-        bool q_ok = false, k_ok = false;                     // this piece's query, this step's K are there
-        long long idle = clock64();
-        while (more || nqk[0] != npv[0] || nqk[1] != npv[1]) {
-          bool did = false;
-          // never waited for: the softmax warps may have to finish a piece first
-          if (want && mbar_test_wait(pfull + np % kRgRing, (np / kRgRing) & 1)) {
-            more = fetch(np++, w, false);
-            want = more && w.count == 0;
-            i = w.lo;
-            did = true;
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (npv[x] == nqk[x] || !mbar_test_wait(pready + x, npv[x] & 1)) continue;
-            tc_fence_after();
-            const int up = (npv[x] & 1) ? step_of[x][1] : step_of[x][0];
-            const bool first = (npv[x] & 1) ? opens[x][1] : opens[x][0];
-            const uint32_t vb = C::BF ? raddr + up * C::RSTAGE + C::PPS * C::PAGE
-                                      : caddr + up * C::CSTAGE + C::PPS * C::CPAGE;
-#pragma unroll
-            for (int j = 0; j < C::PP; ++j)
-#pragma unroll
-              for (int kk = 0; kk < C::PPS; ++kk)
-                mma_f16_ts(tmem + C::COL_O + x * D, tmem + C::COL_P + x * 64 + j * 32 + 8 * kk,
-                           sdesc_plain(vb + kk * C::CPAGE, C::V_LBO, C::V_SBO), id_pv,
-                           (first && j == 0 && kk == 0) ? 0u : 1u);
-            mma_commit(pvdone + x);
-            ++npv[x];
-            did = true;
-            bool last = false;
-#pragma unroll
-            for (int j = 0; j < C::NC; ++j)
-              if (j == up) last = --open[j] == 0;
-            if (last) mma_commit(C::BF ? rfree + up : cfree + up);   // the stage is free
-          }
-          if (more && !want) {
-            const bool two = w.rows > 128;
-            const int x = two ? half : (i - w.lo) & 1;
-            if (!q_ok) q_ok = mbar_test_wait(qready, pc & 1);
-            if (q_ok && !k_ok) k_ok = mbar_test_wait(cfull + stage, (u / C::NC) & 1);
-            const uint32_t n = x ? nqk[1] : nqk[0], v = x ? npv[1] : npv[0];
-            // S of the slot's last product has been read; at most one P is due
-            if (k_ok && n - v < 2 && (n == 0 || mbar_test_wait(sfree + x, (n - 1) & 1))) {
-              tc_fence_after();
-              const uint32_t kb = C::BF ? raddr + stage * C::RSTAGE : caddr + stage * C::CSTAGE;
-              const uint32_t qa = qaddr + (two ? x : 0) * C::QBYTES;
-#pragma unroll
-              for (int qp = 0; qp < C::QP; ++qp)
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  mma_ss<0>(tmem + C::COL_S + x * 64,
-                            sdesc_plain(qa + qp * C::QBYTES + kk * 256, C::Q_LBO, C::Q_SBO),
-                            sdesc_plain(kb + kk * 256, C::K_LBO, C::K_SBO), id_s, (qp | kk) ? 1u : 0u);
-              mma_commit(sfull + x);
-              const bool opening = two ? i == w.lo : i - w.lo < 2;
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (y == x) {
-                  if (nqk[y] & 1) { step_of[y][1] = stage; opens[y][1] = opening; }
-                  else { step_of[y][0] = stage; opens[y][0] = opening; }
-                  ++nqk[y];
-                }
-              if (half == 0) {
-#pragma unroll
-                for (int j = 0; j < C::NC; ++j)
-                  if (j == stage) open[j] = two ? 2 : 1;
-              }
-              did = true;
-              if (two && half == 0) {
-                half = 1;
-              } else {
-                half = 0;
-                k_ok = false;
-                ++u;
-                stage = stage + 1 == C::NC ? 0 : stage + 1;
-                if (++i >= w.hi) {
-                  want = true;
-                  ++pc;
-                  q_ok = false;
-                }
-              }
-            }
-          }
-          if (did) {
-            idle = clock64();
-          } else {
-            if (*abort_flag) break;
-            if (clock64() - idle > wait_limit) {
-              *abort_flag = 1;
-              break;
-            }
-          }
+      // The whole warp runs through the products (its control flow and the
+      // descriptors stay warp-uniform, which keeps a product at a few
+      // instructions) and one elected lane issues them. Order of a step i:
+      //   two blocks of rows  S_A(i), O_A(i-1), S_B(i), O_B(i-1)
+      //   one                 S_x(i), O_y(i-1)   (x, y the slots of the steps)
+      // so that a slot's next scores are in the making while its softmax warps
+      // are still at work on the last ones.
+      constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
+      constexpr uint32_t id_pv = idesc_f16(D, C::BF);
+      // operand stages: K pages, then V pages
+      const uint32_t q_lo = rg_desc_lo<C::Q_LBO>(smem_u32(qop));
+      const uint32_t k_lo = rg_desc_lo<C::K_LBO>(smem_u32(C::BF ? raw : cst));
+      const uint32_t v_lo = rg_desc_lo<C::V_LBO>(smem_u32(C::BF ? raw : cst) + C::PPS * C::CPAGE);
+      constexpr uint32_t STAGE16 = (C::BF ? C::RSTAGE : C::CSTAGE) / 16;
+      const bool lead = elect_one();
+      uint32_t par_c = 0, par_q = 0;                       // phases of cfull (bit per stage), qready
+      uint32_t par_s = 0, par_p = 0;                       // sfree, pready (bit per slot)
+      uint32_t fresh = 3;                                  // slots whose S has never been written
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wait_limit));
+      };
+      auto scores = [&](int x, int stage, int qx) -> bool {
+        if (fresh & (1u << x)) {
+          fresh &= ~(1u << x);
+        } else {
+          if (!wait(sfree + x, (par_s >> x) & 1u)) return false;
+          par_s ^= 1u << x;
         }
-        // every product issued completes before tensor memory is released
+        tc_fence_after();
+        if (lead) {
+          const uint32_t kb = k_lo + uint32_t(stage) * STAGE16;
+          const uint32_t qa = q_lo + uint32_t(qx) * (C::QBYTES / 16), ds = tmem + C::COL_S + x * 64;
+#pragma unroll
+          for (int qp = 0; qp < C::QP; ++qp)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              rg_mma_ss<rg_desc_hi<C::Q_SBO>(), rg_desc_hi<C::K_SBO>()>(
+                  ds, qa + qp * (C::QBYTES / 16) + kk * 16, kb + kk * 16, id_s, (qp | kk) ? 1u : 0u);
+          mma_commit(sfull + x);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto values = [&](int x, int stage, bool first, bool frees) -> bool {
+        if (!wait(pready + x, (par_p >> x) & 1u)) return false;
+        par_p ^= 1u << x;
+        tc_fence_after();
+        if (lead) {
+          const uint32_t vb = v_lo + uint32_t(stage) * STAGE16;
+          const uint32_t od = tmem + C::COL_O + x * D, pa = tmem + C::COL_P + x * 64;
+#pragma unroll
+          for (int j = 0; j < C::PP; ++j)
+#pragma unroll
+            for (int kk = 0; kk < C::PPS; ++kk)
+              rg_mma_ts<rg_desc_hi<C::V_SBO>()>(od, pa + j * 32 + 8 * kk, vb + kk * (C::CPAGE / 16), id_pv,
+                                                (j | kk) ? 1u : uint32_t(!first));
+          mma_commit(pvdone + x);
+          if (frees) mma_commit(C::BF ? rfree + stage : cfree + stage);   // the step's last product
+        }
+        __syncwarp();
+        return true;
+      };
+      int stage = 0;
+      RgItem w;
+      for (int np = 0; ok && fetch(np, w, true); ++np) {
+        const int steps = __shfl_sync(0xffffffffu, w.hi - w.lo, 0);
+        if (steps == 0) continue;
+        const bool two = __shfl_sync(0xffffffffu, int(w.rows > 128), 0) != 0;
+        ok = wait(qready, par_q);
+        par_q ^= 1u;
+        int last = 0;                                      // the stage of the step before
+        for (int i = 0; ok && i < steps; ++i) {
+          ok = wait(cfull + stage, (par_c >> stage) & 1u);
+          if (!ok) break;
+          par_c ^= 1u << stage;
+          if (two) {
+            ok = scores(0, stage, 0);
+            if (ok && i > 0) ok = values(0, last, i == 1, false);
+            if (ok) ok = scores(1, stage, 1);
+            if (ok && i > 0) ok = values(1, last, i == 1, true);
+          } else {
+            ok = scores(i & 1, stage, 0);
+            if (ok && i > 0) ok = values((i & 1) ^ 1, last, i <= 2, true);
+          }
+          last = stage;
+          stage = stage + 1 == C::NC ? 0 : stage + 1;
+        }
+        if (ok && two) ok = values(0, last, steps == 1, false) && values(1, last, steps == 1, true);
+        if (ok && !two) ok = values((steps - 1) & 1, last, steps <= 2, true);
+      }
+      // every product issued completes before tensor memory is released
+      if (lead) {
         volatile int no_abort = 0;
         mma_commit(drain);
         mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
       }
+      __syncwarp();
     } else if (warp == 2 && lane == 0) {
       // ---------------------------------------------------------- the pieces
       RgWalk w;
@@ -996,7 +1008,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        const uint32_t cma = smem_u32(cst) + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE);
+        // the tokens' factors: [a][b][sv][zv] of 64, four tokens at a time
+        const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const uint32_t pages_ok = cmask[3 * ck].x;
         const uint4 wl = cmask[3 * ck + 1], wh = cmask[3 * ck + 2];
         const uint32_t wild0 = wl.x | wl.y | wl.z | wl.w, wild1 = wh.x | wh.y | wh.z | wh.w;
@@ -1014,9 +1027,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             x2[k] = __fmul2_rn(s0, k2);
             x2[k + 1] = __fmul2_rn(s1, k2);
           } else {
-            const float4 a = lds_f4(cma + 8 * k);
+            const float4 a = cm4[k / 2];
             if constexpr (C::ZP) {
-              const float4 b = lds_f4(cma + 4 * C::ST + 8 * k);
+              const float4 b = cm4[C::ST / 4 + k / 2];
               x2[k] = __ffma2_rn(s0, make_float2(a.x, a.y), __fmul2_rn(make_float2(b.x, b.y), qs2));
               x2[k + 1] = __ffma2_rn(s1, make_float2(a.z, a.w), __fmul2_rn(make_float2(b.z, b.w), qs2));
             } else {
@@ -1052,7 +1065,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           mt = fmaxf(m0, m1) * down;
         }
         if constexpr (C::F8 || C::ZP) {
-          const float4 lt = lds_f4(cma + 16 * C::ST);      // log2 of the largest V scales
+          const float4 lt = cm4[C::ST];      // log2 of the largest V scales
           mt += fmaxf(lt.x, lt.y);
         }
         const bool move = mt > m_run + 8.f;
@@ -1087,10 +1100,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           for (int k = 0; k < 16; ++k) {
             const int kk = 16 * hf + k;
             if constexpr (C::F8 || C::ZP) {
-              if ((k & 1) == 0) sv4 = lds_f4(cma + 8 * C::ST + 8 * kk);
+              if ((k & 1) == 0) sv4 = cm4[C::ST / 2 + kk / 2];
             }
             if constexpr (C::ZP) {
-              if ((k & 1) == 0) zv4 = lds_f4(cma + 12 * C::ST + 8 * kk);
+              if ((k & 1) == 0) zv4 = cm4[3 * C::ST / 4 + kk / 2];
             }
             const float2 e = __ffma2_rn(x2[kk], dn2, nm2);
             const float2 p2 = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
