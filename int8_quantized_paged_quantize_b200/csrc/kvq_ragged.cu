@@ -63,11 +63,11 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
   b.B = a.n_seqs;
   b.T = a.total_q;
   b.Hk = d.n_kv_heads;
-  b.G = G;
   b.W = d.max_blocks_per_seq;
   b.max_ctx = a.max_ctx;
-  b.window = a.window;
-  b.pos_per_block = C::RPB / G;
+  b.p.g_log = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
+  b.p.pos_log = (C::RPB == 256 ? 8 : 7) - b.p.g_log;
+  b.p.window = a.window;
   const int grid = device_sm_count();                    // one CTA per SM
   e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kRgThreads), C::SMEM, st,
                  static_cast<const __nv_bfloat16*>(a.q), a.q_stride, static_cast<const uint8_t*>(a.kc),
@@ -75,9 +75,9 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
                  static_cast<const __nv_bfloat16*>(a.vs), a.tables, b, int(d.num_blocks),
                  a.sm_scale * kLog2e, per_tensor, decode_wait_limit(), a.out, po, pml, pieces, w.rows);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(ragged_merge_kernel<D, OutT>, dim3(unsigned(grid), unsigned((std::min(w.rows, C::RPB) + 7) / 8)),
+  e = launch_pdl(ragged_merge_kernel<D, OutT>, dim3(unsigned(grid), unsigned((std::min(w.rows, C::RPB) + 31) / 32)),
                  dim3(256), 0, st, static_cast<const float*>(po), static_cast<const float*>(pml),
-                 static_cast<const RgPiece*>(pieces), grid, w.rows, b.pos_per_block, G, int(d.n_q_heads),
+                 static_cast<const RgPiece*>(pieces), grid, w.rows, b.p, int(d.n_q_heads),
                  static_cast<OutT*>(a.out));
   return e;
 }

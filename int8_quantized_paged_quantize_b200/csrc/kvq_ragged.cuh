@@ -125,7 +125,8 @@ struct __align__(16) RgItem {
 struct RgBatch {
   const int32_t* cu;
   const int32_t* ctx_lens;
-  int B, T, Hk, G, W, max_ctx, window, pos_per_block;
+  int B, T, Hk, W, max_ctx;
+  RgShape p;
 
   // sequence b: its new tokens and context; a range or a context that is not
   // legal counts as empty
@@ -161,15 +162,15 @@ struct RgWalk {
     nb = 0;
     while (b < a.B) {
       s = a.seq(b, &row0, nullptr);
-      nb = rg_blocks(s, a.pos_per_block);
+      nb = rg_blocks(s, a.p);
       if (nb > 0) return;
       ++b;
     }
   }
   __device__ __forceinline__ int weight() const { return rows > 128 ? 2 : 1; }
   __device__ __forceinline__ bool item(const RgBatch& a) {
-    rg_block(s, k, a.pos_per_block, a.window, &first, &count);
-    rows = rg_rows(s, k, a.pos_per_block, a.G);
+    rg_block(s, k, a.p, &first, &count);
+    rows = rg_rows(s, k, a.p);
     return rg_piece(pos, count, weight(), start, end, &lo, &hi);
   }
   __device__ __forceinline__ void step(const RgBatch& a) {
@@ -200,11 +201,11 @@ struct RgWalk {
     start = start_;
     end = end_;
     load(a);
-    const long long L = rg_cost(s, a.pos_per_block, a.G, a.window);
-    const long long off = start - P0 * a.Hk;
-    h = int(off / L);
-    k = rg_find(s, off - h * L, a.pos_per_block, a.G, a.window);
-    pos = P0 * a.Hk + h * L + rg_prefix(s, k, a.pos_per_block, a.G, a.window);
+    const long long L = rg_cost(s, a.p);
+    long long off = start - P0 * a.Hk;
+    for (h = 0; off >= L; ++h) off -= L;
+    k = nb > 1 ? rg_find(s, off, a.p) : 0;
+    pos = start - off + (k > 0 ? rg_prefix(s, k, a.p) : 0);
     settle(a);
   }
   __device__ __forceinline__ void next(const RgBatch& a) {
@@ -263,6 +264,10 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
 }
 __device__ __forceinline__ void sts_u4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t rg_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 // One arrival for the whole warp, after what its lanes did.
@@ -389,66 +394,56 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
   grid_dep_launch_dependents();
 
   // ------------------------------------------------------------ the share
-  long long T = 0;                             // cost of the whole list
-  {
-    long long sum = 0;
-    for (int bb = threadIdx.x; bb < bt.B; bb += blockDim.x) {
+  // Each thread has one sequence (or, in rounds, every 512th): its cost, the
+  // sum before it, and with that whether the share begins in it.
+  long long T = 0;                             // cost per KV head of the whole list
+  long long mine = 0, before = 0;              // of this thread's sequence in the last round
+  if (threadIdx.x < 2) pieces[2 * blockIdx.x + threadIdx.x].valid = 0;
+  auto round = [&](int base, bool check) {
+    const int bb = base + threadIdx.x;
+    mine = 0;
+    if (bb < bt.B) {
       int row0;
       unsigned bad;
       const RgSeq s = bt.seq(bb, &row0, &bad);
-      if (bad && blockIdx.x == 0) flag_error(bad);
-      sum += rg_cost(s, bt.pos_per_block, bt.G, bt.window);
+      if (check && bad && blockIdx.x == 0) flag_error(bad);
+      mine = rg_cost(s, bt.p);
     }
+    long long incl = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red64[warp] = sum;
-    if (threadIdx.x < 2) pieces[2 * blockIdx.x + threadIdx.x].valid = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) red64[warp] = incl;
     __syncthreads();
+    before = T + incl - mine;
 #pragma unroll
-    for (int w = 0; w < NWARPS; ++w) T += red64[w];
-    T *= bt.Hk;
-  }
-  const long long N = ll_min((long long)gridDim.x, ll_max(1, T / kRgMinShare));
-  if (T == 0 || blockIdx.x >= N) {             // uniform for the CTA
+    for (int w = 0; w < NWARPS; ++w) {
+      const long long x = red64[w];
+      before += w < warp ? x : 0;
+      T += x;
+    }
+    __syncthreads();
+  };
+  for (int base = 0; base < bt.B; base += kRgThreads) round(base, true);
+  const long long all = T * bt.Hk;
+  const long long N = ll_min((long long)gridDim.x, ll_max(1, all / kRgMinShare));
+  if (all == 0 || blockIdx.x >= N) {           // uniform for the CTA
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     return;
   }
-  const long long start = (blockIdx.x * T) / N, end = ((blockIdx.x + 1) * T) / N;
-  {
-    // the sequence that holds cost position `start`
-    long long run = 0;
-    for (int base = 0; base < bt.B; base += blockDim.x) {
-      const int bb = base + threadIdx.x;
-      long long c = 0;
-      if (bb < bt.B) {
-        int row0;
-        c = rg_cost(bt.seq(bb, &row0, nullptr), bt.pos_per_block, bt.G, bt.window);
-      }
-      long long incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      __syncthreads();
-      if (lane == 31) red64[warp] = incl;
-      __syncthreads();
-      long long before = 0, total = 0;
-#pragma unroll
-      for (int w = 0; w < NWARPS; ++w) {
-        before += w < warp ? red64[w] : 0;
-        total += red64[w];
-      }
-      const long long p0 = run + before + incl - c;
-      if (c > 0 && p0 * bt.Hk <= start && start < (p0 + c) * bt.Hk) {
-        misci[0] = bb;
-        miscll[0] = p0;
-      }
-      run += total;
-      __syncthreads();
-      if (misci[0] >= 0) break;                // uniform
+  const long long start = (blockIdx.x * all) / N, end = ((blockIdx.x + 1) * all) / N;
+  if (bt.B > kRgThreads) T = 0;
+  for (int base = 0; base < bt.B; base += kRgThreads) {
+    if (bt.B > kRgThreads) round(base, false);
+    if (mine > 0 && before * bt.Hk <= start && start < (before + mine) * bt.Hk) {
+      misci[0] = base + threadIdx.x;
+      miscll[0] = before;
     }
   }
+  __syncthreads();
+
   // piece i of the share; false when there is none (or the kernel gave up). By
   // one lane, or by a whole warp (`whole`).
   auto fetch = [&](int i, RgItem& it, bool whole) -> bool {
@@ -545,13 +540,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      // The whole warp runs through the products (its control flow and the
-      // descriptors stay warp-uniform, which keeps a product at a few
-      // instructions) and one elected lane issues them. Order of a step i:
+      // One elected lane issues the products. Order of a step i:
       //   two blocks of rows  S_A(i), O_A(i-1), S_B(i), O_B(i-1)
       //   one                 S_x(i), O_y(i-1)   (x, y the slots of the steps)
       // so that a slot's next scores are in the making while its softmax warps
       // are still at work on the last ones.
+      if (elect_one()) {
       constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
       constexpr uint32_t id_pv = idesc_f16(D, C::BF);
       // operand stages: K pages, then V pages
@@ -559,13 +553,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       const uint32_t k_lo = rg_desc_lo<C::K_LBO>(smem_u32(C::BF ? raw : cst));
       const uint32_t v_lo = rg_desc_lo<C::V_LBO>(smem_u32(C::BF ? raw : cst) + C::PPS * C::CPAGE);
       constexpr uint32_t STAGE16 = (C::BF ? C::RSTAGE : C::CSTAGE) / 16;
-      const bool lead = elect_one();
       uint32_t par_c = 0, par_q = 0;                       // phases of cfull (bit per stage), qready
       uint32_t par_s = 0, par_p = 0;                       // sfree, pready (bit per slot)
       uint32_t fresh = 3;                                  // slots whose S has never been written
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wait_limit));
+        return mbar_wait(bar, parity, abort_flag, wait_limit);
       };
       auto scores = [&](int x, int stage, int qx) -> bool {
         if (fresh & (1u << x)) {
@@ -575,7 +568,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           par_s ^= 1u << x;
         }
         tc_fence_after();
-        if (lead) {
+        {
           const uint32_t kb = k_lo + uint32_t(stage) * STAGE16;
           const uint32_t qa = q_lo + uint32_t(qx) * (C::QBYTES / 16), ds = tmem + C::COL_S + x * 64;
 #pragma unroll
@@ -586,14 +579,13 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   ds, qa + qp * (C::QBYTES / 16) + kk * 16, kb + kk * 16, id_s, (qp | kk) ? 1u : 0u);
           mma_commit(sfull + x);
         }
-        __syncwarp();
         return true;
       };
       auto values = [&](int x, int stage, bool first, bool frees) -> bool {
         if (!wait(pready + x, (par_p >> x) & 1u)) return false;
         par_p ^= 1u << x;
         tc_fence_after();
-        if (lead) {
+        {
           const uint32_t vb = v_lo + uint32_t(stage) * STAGE16;
           const uint32_t od = tmem + C::COL_O + x * D, pa = tmem + C::COL_P + x * 64;
 #pragma unroll
@@ -605,15 +597,14 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           mma_commit(pvdone + x);
           if (frees) mma_commit(C::BF ? rfree + stage : cfree + stage);   // the step's last product
         }
-        __syncwarp();
         return true;
       };
       int stage = 0;
       RgItem w;
-      for (int np = 0; ok && fetch(np, w, true); ++np) {
-        const int steps = __shfl_sync(0xffffffffu, w.hi - w.lo, 0);
+      for (int np = 0; ok && fetch(np, w, false); ++np) {
+        const int steps = w.hi - w.lo;
         if (steps == 0) continue;
-        const bool two = __shfl_sync(0xffffffffu, int(w.rows > 128), 0) != 0;
+        const bool two = w.rows > 128;
         ok = wait(qready, par_q);
         par_q ^= 1u;
         int last = 0;                                      // the stage of the step before
@@ -637,10 +628,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         if (ok && !two) ok = values((steps - 1) & 1, last, steps <= 2, true);
       }
       // every product issued completes before tensor memory is released
-      if (lead) {
-        volatile int no_abort = 0;
-        mma_commit(drain);
-        mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
+      volatile int no_abort = 0;
+      mma_commit(drain);
+      mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
       }
       __syncwarp();
     } else if (warp == 2 && lane == 0) {
@@ -832,7 +822,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     float* xch = reinterpret_cast<float*>(smem + C::OFF_X);              // [16][128]
     float4* xsum = reinterpret_cast<float4*>(smem + C::OFF_XS);          // [128]
     const int pair_bar = 2 + quarter;                      // the two warps of this lane quarter
-    const int gshift = __ffs(bt.G) - 1;
+    const int gshift = bt.p.g_log, G = 1 << gshift;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {  // tcgen05.ld / st are warp-wide
       if (ok) ok = mbar_wait(bar, parity, abort_flag, wait_limit);
@@ -840,83 +830,118 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     };
     // this thread's row of a block: the block row, its token of the sequence's new ones
     auto block_row = [&](const RgItem& w) -> int { return w.rows > 128 ? x * 128 + r : r; };
-    auto token_of = [&](const RgItem& w, int rr) -> int { return w.k * bt.pos_per_block + (rr >> gshift); };
-    auto head_of = [&](const RgItem& w, int rr) -> int { return (w.h << gshift) + (rr & (bt.G - 1)); };
+    auto token_of = [&](const RgItem& w, int rr) -> int { return (w.k << bt.p.pos_log) + (rr >> gshift); };
+    auto head_of = [&](const RgItem& w, int rr) -> int { return (w.h << gshift) + (rr & (G - 1)); };
 
-    // The query row of a piece into the operand (K-major 8-row groups of
-    // 16-byte chunks). `down` takes S back to the row's units, qsum is the sum of
-    // the operand's values (the zero-point term). With one block of rows for
-    // both slots, slot A's warps write it.
+    // The query rows of a piece into the operand (K-major 8-row groups of
+    // 16-byte chunks). A warp takes its 32 rows eight at a time, a lane one row
+    // (lane % 8) of them and every fourth chunk: 64 contiguous bytes a row from
+    // global memory, 512 to shared memory. `down` takes S of this thread's own
+    // row (lane = 8 (lane / 8) + lane % 8) back to the row's units, qsum is the
+    // sum of its operand's values (the zero-point term). With one block of rows
+    // for both slots, slot A's warps write it.
     auto store_q = [&](const RgItem& w, float& down, float& qsum) {
       down = 1.f;
       qsum = 0.f;
       const bool two = w.rows > 128;
-      const int rr = block_row(w);
-      const bool have = rr < w.rows, wr = two || x == 0;
-      uint4 c[D / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          q + int64_t(w.row0 + (have ? token_of(w, rr) : 0)) * q_stride + int64_t(head_of(w, rr)) * D);
+      const int rs = lane & 7, cs = lane >> 3;
+      const bool wr = two || x == 0;
+      constexpr int NI = D / 32;
+      uint4 c[4][NI];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) c[i] = have ? src[i] : make_uint4(0, 0, 0, 0);
-      uint8_t* row = qop + (two ? x : 0) * C::QBYTES + (r >> 3) * C::Q_SBO + (r & 7) * 16;
+      for (int rg = 0; rg < 4; ++rg) {
+        const int rr = (two ? x * 128 : 0) + quarter * 32 + 8 * rg + rs;
+        const bool have = rr < w.rows;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            q + int64_t(w.row0 + (have ? token_of(w, rr) : 0)) * q_stride + int64_t(head_of(w, rr)) * D) + cs;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) c[rg][i] = have ? src[4 * i] : make_uint4(0, 0, 0, 0);
+      }
+      uint8_t* dst = qop + (two ? x : 0) * C::QBYTES + quarter * 4 * C::Q_SBO + rs * 16 + cs * C::Q_LBO;
       if constexpr (C::BF) {
         if (wr) {
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(row + i * C::Q_LBO) = c[i];
+          for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) *reinterpret_cast<uint4*>(dst + rg * C::Q_SBO + 4 * i * C::Q_LBO) = c[rg][i];
         }
       } else {
         // static INT8: q times the K scale of the channel
-        auto scale = [&](int d) -> float {
-          if constexpr (C::SI) return __bfloat162float(ks[per_tensor ? 0 : w.h * D + d]);
-          return 1.f;
-        };
-        float amax = 0.f;
+        uint4 sc[C::SI ? NI : 1];
         if constexpr (C::SI) {
+          const uint32_t one = per_tensor ? *reinterpret_cast<const uint16_t*>(ks) * 0x10001u : 0u;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(v[e]) * scale(8 * i + 2 * e)),
-                                       fabsf(bf16_hi(v[e]) * scale(8 * i + 2 * e + 1))));
-          }
-        } else {
-          uint32_t m = 0u;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            m = vmax_u16x2(m, c[i].x & 0x7fff7fffu);
-            m = vmax_u16x2(m, c[i].y & 0x7fff7fffu);
-            m = vmax_u16x2(m, c[i].z & 0x7fff7fffu);
-            m = vmax_u16x2(m, c[i].w & 0x7fff7fffu);
-          }
-          amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+          for (int i = 0; i < NI; ++i)
+            sc[i] = per_tensor ? make_uint4(one, one, one, one)
+                               : reinterpret_cast<const uint4*>(ks + w.h * D)[4 * i + cs];
         }
-        // power-of-two scaling: the largest element lands in [2^14, 2^15)
-        int e2 = 0;
-        if (amax > 0.f && amax < INFINITY) e2 = 14 - ilogbf(amax);
-        e2 = max(-100, min(100, e2));
-        const float up = __int_as_float((127 + e2) << 23);
-        down = __int_as_float((127 - e2) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = bf16_lo(v[e]) * scale(8 * i + 2 * e) * up;
-            const float b = bf16_hi(v[e]) * scale(8 * i + 2 * e + 1) * up;
-            const __half2 h2 = __floats2half2_rn(a, b);
-            hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
-            if constexpr (C::QP == 2) {
-              const __half2 l2 = __floats2half2_rn(a - __low2float(h2), b - __high2float(h2));
-              lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
-            }
-            if constexpr (C::ZP) qsum += __low2float(h2) + __high2float(h2);
+        auto pair = [&](int rg, int i, int e) -> float2 {
+          const uint32_t v = e == 0 ? c[rg][i].x : e == 1 ? c[rg][i].y : e == 2 ? c[rg][i].z : c[rg][i].w;
+          float2 f = make_float2(bf16_lo(v), bf16_hi(v));
+          if constexpr (C::SI) {
+            const uint32_t k = e == 0 ? sc[i].x : e == 1 ? sc[i].y : e == 2 ? sc[i].z : sc[i].w;
+            f.x *= bf16_lo(k);
+            f.y *= bf16_hi(k);
           }
-          if (wr) {
-            *reinterpret_cast<uint4*>(row + i * C::Q_LBO) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (C::QP == 2)
-              *reinterpret_cast<uint4*>(row + C::QBYTES + i * C::Q_LBO) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          return f;
+        };
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+          float amax = 0.f;
+          if constexpr (C::SI) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = pair(rg, i, e);
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+          } else {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              m = vmax_u16x2(m, c[rg][i].x & 0x7fff7fffu);
+              m = vmax_u16x2(m, c[rg][i].y & 0x7fff7fffu);
+              m = vmax_u16x2(m, c[rg][i].z & 0x7fff7fffu);
+              m = vmax_u16x2(m, c[rg][i].w & 0x7fff7fffu);
+            }
+            amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+          // power-of-two scaling: the largest element lands in [2^14, 2^15)
+          int e2 = 0;
+          if (amax > 0.f && amax < INFINITY) e2 = 14 - ilogbf(amax);
+          e2 = max(-100, min(100, e2));
+          const float up = __int_as_float((127 + e2) << 23);
+          if (rg == cs) down = __int_as_float((127 - e2) << 23);
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = pair(rg, i, e);
+              const float a = f.x * up, b = f.y * up;
+              const __half2 h2 = __floats2half2_rn(a, b);
+              hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              if constexpr (C::QP == 2) {
+                const __half2 l2 = __floats2half2_rn(a - __low2float(h2), b - __high2float(h2));
+                lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
+              }
+              if constexpr (C::ZP) sum += __low2float(h2) + __high2float(h2);
+            }
+            if (wr) {
+              *reinterpret_cast<uint4*>(dst + rg * C::Q_SBO + 4 * i * C::Q_LBO) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              if constexpr (C::QP == 2)
+                *reinterpret_cast<uint4*>(dst + C::QBYTES + rg * C::Q_SBO + 4 * i * C::Q_LBO) =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          if constexpr (C::ZP) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            if (rg == cs) qsum = sum;
           }
         }
       }
@@ -924,20 +949,33 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     };
     using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
     OutT* out = static_cast<OutT*>(out_);
+    const bool wide = (reinterpret_cast<uintptr_t>(out_) & 31) == 0;
+    auto st32 = [&](void* dst, const uint32_t (&v)[8]) {   // 32 bytes of one row
+      if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+    };
     auto store_row16 = [&](OutT* dst, const float (&o)[16]) {
+      uint32_t v[8];
       if constexpr (HP) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(o[8 * i + e]);
+          st32(dst + 8 * i, v);
+        }
       } else {
-        uint32_t wv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-          wv[e] = *reinterpret_cast<const uint32_t*>(&v);
+          const __nv_bfloat162 w2 = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+          v[e] = *reinterpret_cast<const uint32_t*>(&w2);
         }
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+        st32(dst, v);
       }
     };
     // The next piece with steps; blocks in which no row attends anything get
@@ -984,7 +1022,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // tokens lo_t <= t < lim are attended; rows past the block's see everything
       // (nothing of them is written)
       const int lim = row_ok ? max(0, p + 1) : INT_MAX;
-      const int lo_t = row_ok && bt.window > 0 ? max(0, p + 1 - bt.window) : 0;
+      const int lo_t = row_ok && bt.p.window > 0 ? max(0, p + 1 - bt.p.window) : 0;
       float m_run = -INFINITY, l = 0.f, corr = 0.f;
       bool any_step = false;
       for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
@@ -1189,7 +1227,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         const int slot = pw.lo == 0 ? 1 : 0;
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         const int64_t orow = int64_t(pw.row0 + (row_ok ? token_of(pw, rr) : 0)) * (bt.Hk << gshift) + head_of(pw, rr);
-        const int64_t prow = (int64_t(blockIdx.x) * 2 + slot) * rows_cap + rr;
+        const int64_t place = int64_t(blockIdx.x) * 2 + slot;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t ov[16];
@@ -1220,15 +1258,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             if (whole) {
               store_row16(out + orow * D + 16 * c, o);
             } else {
-              float* po = part_o + prow * D + 16 * c;
+              // channel by channel, the rows side by side
+              float* po = part_o + (place * D + 16 * c) * rows_cap + rr;
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(po + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 16; ++e) po[int64_t(e) * rows_cap] = o[e];
             }
           }
         }
         if (!whole && (two || x == 0)) {
-          if (row_ok) *reinterpret_cast<float2*>(part_ml + prow * 2) = make_float2(m_run, l);
+          if (row_ok) *reinterpret_cast<float2*>(part_ml + (place * rows_cap + rr) * 2) = make_float2(m_run, l);
           if (x == 0 && r == 0) rg_record(pieces + 2 * blockIdx.x + slot, pw.hi == pw.count, pw.row0, pw.n, pw.h, pw.k);
         }
         tc_fence_before();
@@ -1257,7 +1295,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       for (int j = threadIdx.x; j < w.rows * D; j += blockDim.x) {
         const int rr = j / D, d = j % D;
         if (w.whole()) {
-          const int64_t row = int64_t(w.row0 + w.k * bt.pos_per_block + rr / bt.G) * (bt.Hk * bt.G) + w.h * bt.G + rr % bt.G;
+          const int64_t row = int64_t(w.row0 + (w.k << bt.p.pos_log) + (rr >> bt.p.g_log)) * (bt.Hk << bt.p.g_log) +
+                              (w.h << bt.p.g_log) + (rr & ((1 << bt.p.g_log) - 1));
           if constexpr (HP) out[row * D + d] = nan;
           else out[row * D + d] = __float2bfloat16_rn(nan);
         } else if (d < 2) {
@@ -1272,14 +1311,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 
 // Joins the pieces of the blocks that were cut: a block's pieces are the second
 // place of the CTA where it begins and the first places of the CTAs after it,
-// up to the one marked last. One warp a row, each lane D/32 channels:
+// up to the one marked last.
 //   m = max m_i, l = sum l_i 2^(m_i - m), out = sum O_i 2^(m_i - m) / l.
 // The order of the pieces is that of the tokens, so the result does not depend
-// on timing.
+// on timing. A CTA takes 32 rows (lane = row), a warp D/8 of the channels; the
+// places hold the rows side by side, so a warp's loads are whole lines.
 template <int D, typename OutT>
 __global__ void __launch_bounds__(256) ragged_merge_kernel(
     const float* part_o, const float* part_ml, const RgPiece* pieces, int n_ctas, int rows_cap,
-    int pos_per_block, int G, int Hq, OutT* __restrict__ out) {
+    RgShape p, int Hq, OutT* __restrict__ out) {
   tc::grid_dep_wait();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   RgPiece pc;
@@ -1290,10 +1330,12 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(
     pc.h = b.x; pc.k = b.y;
   }
   if (!pc.valid) return;
-  const int rr = blockIdx.y * 8 + warp;
-  const int j = pc.k * pos_per_block + rr / G;
-  if (rr >= rows_cap || rr >= pos_per_block * G || j >= pc.n) return;
-  // how many pieces follow: the first place marked last, 32 CTAs at a time
+  RgSeq sq;
+  sq.n = pc.n;
+  sq.ctx = 0;
+  const int rows = rg_rows(sq, pc.k, p);
+  if (blockIdx.y * 32 >= rows) return;
+  // how many pieces follow: up to the first place marked last, 32 CTAs at a time
   int n = 0;
   for (int base = c0 + 1; base < n_ctas; base += 32) {
     const int c = base + lane;
@@ -1307,36 +1349,38 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(
     }
     n += 32;
   }
-  const int total = n + 1;
-  auto place = [&](int i) -> int64_t { return (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * rows_cap + rr; };
-  float m = -INFINITY;
-  for (int i = lane; i < total; i += 32) m = fmaxf(m, __ldcg(part_ml + place(i) * 2));
-  m = warp_max(m);
-  if (m == -INFINITY) m = 0.f;
-  constexpr int NV = D / 32;
+  const int total = n + 1, rr = blockIdx.y * 32 + lane;
+  if (rr >= rows) return;
+  auto place = [&](int i) -> int64_t { return int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+  constexpr int NV = D / 8, U = 4;             // channels a thread; pieces in flight
   float o[NV] = {};
-  float l = 0.f;
-  for (int base = 0; base < total; base += 8) {
-    float2 ml[8];
-    float v[8][NV];
+  float m = -INFINITY, l = 0.f;
+  for (int base = 0; base < total; base += U) {
+    float2 ml[U];
+    float v[U][NV];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < U; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
       if (base + i < total) {
         const int64_t pl = place(base + i);
-        ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml + pl * 2));
-        if constexpr (NV == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(part_o + pl * D) + lane);
-          v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(part_o + pl * D) + lane);
-          v[i][0] = f.x; v[i][1] = f.y;
-        }
+        ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + pl * rows_cap + rr);
+        const float* src = part_o + (pl * D + warp * NV) * rows_cap + rr;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) v[i][e] = __ldcg(src + int64_t(e) * rows_cap);
       }
     }
+    float mn = m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < U; ++i) mn = fmaxf(mn, ml[i].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, keep = exp2f(m - ref);
+    m = mn;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < NV; ++e) o[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
       if (base + i < total) {
-        const float w = exp2f(ml[i].x - m);
+        const float w = exp2f(ml[i].x - ref);
         l += ml[i].y * w;
 #pragma unroll
         for (int e = 0; e < NV; ++e) o[e] += v[i][e] * w;
@@ -1344,16 +1388,18 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  OutT* dst = out + (int64_t(pc.row0 + j) * Hq + pc.h * G + rr % G) * D + lane * NV;
-#pragma unroll
-  for (int e = 0; e < NV; ++e) o[e] *= inv;
+  const int G = 1 << p.g_log;
+  OutT* dst = out + (int64_t(pc.row0 + (pc.k << p.pos_log) + (rr >> p.g_log)) * Hq + pc.h * G + (rr & (G - 1))) * D + warp * NV;
   if constexpr (sizeof(OutT) == 4) {
-    if constexpr (NV == 4) *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-    else *reinterpret_cast<float2*>(dst) = make_float2(o[0], o[1]);
+#pragma unroll
+    for (int e = 0; e < NV; e += 4)
+      *reinterpret_cast<float4*>(dst + e) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
   } else {
 #pragma unroll
-    for (int e = 0; e < NV; e += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(o[e], o[e + 1]);
+    for (int e = 0; e < NV; e += 8)
+      *reinterpret_cast<uint4*>(dst + e) =
+          make_uint4(rg_pack(o[e] * inv, o[e + 1] * inv), rg_pack(o[e + 2] * inv, o[e + 3] * inv),
+                     rg_pack(o[e + 4] * inv, o[e + 5] * inv), rg_pack(o[e + 6] * inv, o[e + 7] * inv));
   }
 }
 

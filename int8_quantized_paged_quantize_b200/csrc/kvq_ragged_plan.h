@@ -30,72 +30,82 @@ struct RgSeq {
   int n, ctx;
 };
 
+// The shape of a block: pos = 1 << pos_log tokens of the sequence's new ones, G = 1 << g_log
+// query heads each. All sizes are powers of two, so that the list needs no division.
+struct RgShape {
+  int pos_log, g_log, window;
+};
+
 // Steps [first, first + count) that block k reads: tokens from the first row's
 // window (window 0: all) to the last row's own position.
-KVQ_HD void rg_block(const RgSeq& s, int k, int pos_per_block, int window, int* first, int* count) {
+KVQ_HD void rg_block(const RgSeq& s, int k, const RgShape& p, int* first, int* count) {
   const int base = s.ctx - s.n;
-  const int j0 = k * pos_per_block;
-  const int j1 = s.n - j0 < pos_per_block ? s.n : j0 + pos_per_block;
+  const int j0 = k << p.pos_log;
+  const int j1 = s.n - j0 < (1 << p.pos_log) ? s.n : j0 + (1 << p.pos_log);
   const int end = base + j1;
   if (end <= 0) {
     *first = *count = 0;
     return;
   }
-  int beg = window > 0 ? base + j0 + 1 - window : 0;
+  int beg = p.window > 0 ? base + j0 + 1 - p.window : 0;
   if (beg < 0) beg = 0;
-  *first = beg / kRgStep;
-  *count = (end - 1) / kRgStep + 1 - *first;
+  *first = beg >> 6;
+  *count = ((end - 1) >> 6) + 1 - *first;
 }
 
-KVQ_HD int rg_rows(const RgSeq& s, int k, int pos_per_block, int G) {
-  const int left = s.n - k * pos_per_block;
-  return (left < pos_per_block ? left : pos_per_block) * G;
+KVQ_HD int rg_rows(const RgSeq& s, int k, const RgShape& p) {
+  const int left = s.n - (k << p.pos_log);
+  return (left < (1 << p.pos_log) ? left : 1 << p.pos_log) << p.g_log;
 }
 
-// sum over k < m of ceil(max(0, a + k P) / 64); P divides 64 or is a multiple of it.
-KVQ_HD long long rg_sum_ceil(int a, int P, long long m) {
-  long long k1 = a > 0 ? 0 : (-(long long)a) / P + 1;   // first positive term
+// Q(n) = sum of ceil(i / 2^r) over i = 1 .. n.
+KVQ_HD long long rg_q(long long n, int r) {
+  const long long q = n >> r;
+  return ((q * (q + 1) / 2) << r) + (n - (q << r)) * (q + 1);
+}
+
+// sum over k < m of ceil(max(0, a + (k << pos_log)) / 64).
+KVQ_HD long long rg_sum_ceil(int a, int pos_log, long long m) {
+  const long long k1 = a > 0 ? 0 : ((-(long long)a) >> pos_log) + 1;   // first positive term
   if (k1 >= m) return 0;
-  const long long x = a + k1 * P, c = m - k1;
-  if (P >= kRgStep) return c * ((x + kRgStep - 1) / kRgStep) + (P / kRgStep) * (c * (c - 1) / 2);
-  const long long r = kRgStep / P, h = (x + P - 1) / P;
-  // ceil((x + k P) / 64) = ceil((h + k) / r); Q(n) = sum of ceil(i / r), i = 1 .. n
-  const long long n1 = h + c - 1, n0 = h - 1;
-  const long long q1 = n1 / r, q0 = n0 / r;
-  return (r * (q1 * (q1 + 1) / 2) + (n1 % r) * (q1 + 1)) - (r * (q0 * (q0 + 1) / 2) + (n0 % r) * (q0 + 1));
+  const long long x = a + (k1 << pos_log), c = m - k1;
+  if (pos_log >= 6) return c * ((x + 63) >> 6) + ((c * (c - 1) / 2) << (pos_log - 6));
+  // ceil((x + (k << pos_log)) / 64) = ceil((h + k) / 2^r)
+  const int r = 6 - pos_log;
+  const long long h = (x + (1 << pos_log) - 1) >> pos_log;
+  return rg_q(h + c - 1, r) - rg_q(h - 1, r);
 }
 
 // Cost of blocks 0 .. k-1 of a sequence, all of them full (k < number of blocks).
-KVQ_HD long long rg_prefix(const RgSeq& s, int k, int pos_per_block, int G, int window) {
+KVQ_HD long long rg_prefix(const RgSeq& s, int k, const RgShape& p) {
   const int base = s.ctx - s.n;
-  const int w = pos_per_block * G > 128 ? 2 : 1;
-  long long steps = rg_sum_ceil(base + pos_per_block, pos_per_block, k);
+  long long steps = rg_sum_ceil(base + (1 << p.pos_log), p.pos_log, k);
   // floor(x / 64) = ceil((x - 63) / 64)
-  if (window > 0) steps -= rg_sum_ceil(base + 1 - window - (kRgStep - 1), pos_per_block, k);
-  return (long long)k * kRgPiece + w * steps;
+  if (p.window > 0) steps -= rg_sum_ceil(base + 1 - p.window - (kRgStep - 1), p.pos_log, k);
+  return (long long)k * kRgPiece + (steps << (p.pos_log + p.g_log > 7 ? 1 : 0));
 }
 
-KVQ_HD int rg_blocks(const RgSeq& s, int pos_per_block) { return (s.n + pos_per_block - 1) / pos_per_block; }
+KVQ_HD int rg_blocks(const RgSeq& s, const RgShape& p) { return int(((long long)s.n + (1 << p.pos_log) - 1) >> p.pos_log); }
 
-KVQ_HD long long rg_block_cost(const RgSeq& s, int k, int pos_per_block, int G, int window) {
+KVQ_HD long long rg_block_cost(const RgSeq& s, int k, const RgShape& p) {
   int first, count;
-  rg_block(s, k, pos_per_block, window, &first, &count);
-  return kRgPiece + (long long)(rg_rows(s, k, pos_per_block, G) > 128 ? 2 : 1) * count;
+  rg_block(s, k, p, &first, &count);
+  return kRgPiece + (rg_rows(s, k, p) > 128 ? 2LL : 1LL) * count;
 }
 
 // Cost of all blocks of one (sequence, KV head).
-KVQ_HD long long rg_cost(const RgSeq& s, int pos_per_block, int G, int window) {
-  const int nb = rg_blocks(s, pos_per_block);
+KVQ_HD long long rg_cost(const RgSeq& s, const RgShape& p) {
+  const int nb = rg_blocks(s, p);
   if (nb == 0) return 0;
-  return rg_prefix(s, nb - 1, pos_per_block, G, window) + rg_block_cost(s, nb - 1, pos_per_block, G, window);
+  return (nb > 1 ? rg_prefix(s, nb - 1, p) : 0) + rg_block_cost(s, nb - 1, p);
 }
 
 // The block that holds cost position x of the (sequence, KV head)'s blocks.
-KVQ_HD int rg_find(const RgSeq& s, long long x, int pos_per_block, int G, int window) {
-  int lo = 0, hi = rg_blocks(s, pos_per_block);         // prefix(lo) <= x < prefix(hi)
+KVQ_HD int rg_find(const RgSeq& s, long long x, const RgShape& p) {
+  int lo = 0, hi = rg_blocks(s, p);                     // prefix(lo) <= x < prefix(hi)
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
-    if (rg_prefix(s, mid, pos_per_block, G, window) <= x) lo = mid;
+    if (rg_prefix(s, mid, p) <= x) lo = mid;
     else hi = mid;
   }
   return lo;
