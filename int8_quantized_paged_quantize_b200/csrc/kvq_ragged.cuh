@@ -103,8 +103,8 @@ struct RgCfg {
   static constexpr int OFF_XS = OFF_X + 16 * 128 * 4;            // float4 [128]: m, l, corr of slot B
   static constexpr int OFF_BAR = OFF_XS + 128 * 16;
   static constexpr int NBAR = 2 * NRAW + 2 * NC + 8 + 2 + 2 * kRgRing;
-  static constexpr int OFF_MASK = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;   // raw page masks [NRAW], then [NC][12]
-  static constexpr int OFF_RED = OFF_MASK + 16 * ((NRAW + 3) / 4) + 48 * NC;
+  static constexpr int OFF_MASK = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;   // page masks [NRAW], [NC], then [NC][12]
+  static constexpr int OFF_RED = OFF_MASK + 16 * ((NRAW + NC + 3) / 4) + 48 * NC;
   static constexpr int OFF_MISC = OFF_RED + 128;
   static constexpr int OFF_ITEM = OFF_MISC + 48;                 // RgItem [kRgRing]
   static constexpr int USED = OFF_ITEM + kRgRing * 64;
@@ -273,7 +273,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 // One arrival for the whole warp, after what its lanes did.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
-  if (lane == 0) tc::mbar_arrive(bar);
+  // predicated, not branched around
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(tc::smem_u32(bar)),
+      "r"(lane)
+      : "memory");
 }
 
 // A product must cost the thread that issues it few instructions (the 64-bit
@@ -344,9 +349,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
   uint64_t* pfree = pfull + kRgRing;          // [kRgRing] every role has read it
   RgItem* items = reinterpret_cast<RgItem*>(smem + C::OFF_ITEM);
   volatile uint32_t* rmask = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MASK);
-  // per operand stage: {valid pages}, {not-finite V tokens 0..31}, {.. 32..63} as
-  // each converter warp saw them
-  uint4* cmask = reinterpret_cast<uint4*>(smem + C::OFF_MASK + 16 * ((C::NRAW + 3) / 4));
+  // per operand stage, as each converter warp saw them: {whether some page is
+  // missing or some V is not finite}, {not-finite V tokens 0..31}, {.. 32..63}
+  volatile uint32_t* cpages = rmask + C::NRAW;   // [NC] valid pages of an operand stage
+  uint4* cmask = reinterpret_cast<uint4*>(smem + C::OFF_MASK + 16 * ((C::NRAW + C::NC + 3) / 4));
   long long* red64 = reinterpret_cast<long long*>(smem + C::OFF_RED);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -664,6 +670,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         ok = __all_sync(0xffffffffu, ok);                  // what follows votes and reduces over the warp
         const uint32_t pm = rmask[s];
         const int tok0 = (w.first + i) * C::ST;
+        if (ct == 0) cpages[cs] = pm;
         uint8_t* rk = raw + s * C::RSTAGE;
         uint8_t* rv = rk + C::PPS * C::PAGE;
         uint8_t* cb = cst + cs * C::CSTAGE;
@@ -677,7 +684,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           if constexpr (C::BF) {
             // V as it is stored: tokens that hold nothing, and tokens with a NaN
             // or an infinity, are zeroed
-            if (ct == 0) cmw[0] = pm;
             uint32_t bad0 = 0u, bad1 = 0u;
             constexpr int NIT = C::PPS * 2 * D / 128;
 #pragma unroll 4
@@ -714,6 +720,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             bad0 = __reduce_or_sync(0xffffffffu, bad0);
             bad1 = __reduce_or_sync(0xffffffffu, bad1);
             if (lane == 0) {
+              cmw[ct >> 5] = (pm ^ 0xFu) | bad0 | bad1;
               cmw[4 + (ct >> 5)] = bad0;
               cmw[8 + (ct >> 5)] = bad1;
             }
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               if ((ct & 31) == 0) {
                 cm[4 * C::ST + (ct >> 5)] = top > 0.f ? fmaxf(__log2f(top), -64.f) : -64.f;
                 cmw[ct < 32 ? 4 : 9] = wm;
-                if (ct == 0) cmw[0] = pm;
+                cmw[ct >> 5] = (pm ^ 0xFu) | wm;
               }
             }
 #pragma unroll
@@ -836,7 +843,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     // The query rows of a piece into the operand (K-major 8-row groups of
     // 16-byte chunks). A warp takes its 32 rows eight at a time, a lane one row
     // (lane % 8) of them and every fourth chunk: 64 contiguous bytes a row from
-    // global memory, 512 to shared memory. `down` takes S of this thread's own
+    // global memory, 512 to shared memory. `down` takes the scores of this thread's own
     // row (lane = 8 (lane / 8) + lane % 8) back to the row's units, qsum is the
     // sum of its operand's values (the zero-point term). With one block of rows
     // for both slots, slot A's warps write it.
@@ -858,12 +865,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         for (int i = 0; i < NI; ++i) c[rg][i] = have ? src[4 * i] : make_uint4(0, 0, 0, 0);
       }
       uint8_t* dst = qop + (two ? x : 0) * C::QBYTES + quarter * 4 * C::Q_SBO + rs * 16 + cs * C::Q_LBO;
+      // without a scale per token, sm_scale is the row factor's (its sign the query's)
       if constexpr (C::BF) {
+        down = fabsf(qk_scale);
+        const uint32_t sg = qk_scale < 0.f ? 0x80008000u : 0u;
         if (wr) {
 #pragma unroll
           for (int rg = 0; rg < 4; ++rg)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) *reinterpret_cast<uint4*>(dst + rg * C::Q_SBO + 4 * i * C::Q_LBO) = c[rg][i];
+            for (int i = 0; i < NI; ++i)
+              *reinterpret_cast<uint4*>(dst + rg * C::Q_SBO + 4 * i * C::Q_LBO) =
+                  make_uint4(c[rg][i].x ^ sg, c[rg][i].y ^ sg, c[rg][i].z ^ sg, c[rg][i].w ^ sg);
         }
       } else {
         // static INT8: q times the K scale of the channel
@@ -913,8 +925,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           int e2 = 0;
           if (amax > 0.f && amax < INFINITY) e2 = 14 - ilogbf(amax);
           e2 = max(-100, min(100, e2));
-          const float up = __int_as_float((127 + e2) << 23);
+          float up = __int_as_float((127 + e2) << 23);
           if (rg == cs) down = __int_as_float((127 - e2) << 23);
+          if constexpr (C::SI) {
+            up = copysignf(up, qk_scale);
+            if (rg == cs) down *= fabsf(qk_scale);
+          }
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
@@ -1023,14 +1039,25 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // (nothing of them is written)
       const int lim = row_ok ? max(0, p + 1) : INT_MAX;
       const int lo_t = row_ok && bt.p.window > 0 ? max(0, p + 1 - bt.p.window) : 0;
-      float m_run = -INFINITY, l = 0.f, corr = 0.f;
+      const int lim_min = __reduce_min_sync(0xffffffffu, lim), lo_max = __reduce_max_sync(0xffffffffu, lo_t);
+      float m_run = -INFINITY, mref = 0.f, l = 0.f, corr = 0.f;   // mref: m_run, or 0 where it is -inf
       bool any_step = false;
+      // operand stage, and its phase, of this slot's first step
+      int stage = (two ? u0 : u0 + x) % C::NC;
+      uint32_t phase = ((two ? u0 : u0 + x) / C::NC) & 1;
       for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
-        const int u = u0 + i, ck = u % C::NC;
+        const int ck = stage;
+        const uint32_t cpar = phase;
+        const int ahead = two ? 1 : 2;                     // to this slot's next step
+        stage += ahead;
+        if (stage >= C::NC) {
+          stage -= C::NC;
+          phase ^= 1u;
+        }
         // both at once: they are mostly complete
-        if (!__all_sync(0xffffffffu, mbar_test_wait(sfull + x, cnt & 1) & mbar_test_wait(cfull + ck, (u / C::NC) & 1))) {
+        if (!__all_sync(0xffffffffu, mbar_test_wait(sfull + x, cnt & 1) & mbar_test_wait(cfull + ck, cpar))) {
           wait_all(sfull + x, cnt & 1);
-          wait_all(cfull + ck, (u / C::NC) & 1);
+          wait_all(cfull + ck, cpar);
         }
         tc_fence_after();
         if (!active) {
@@ -1048,31 +1075,41 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         warp_arrive(sfree + x, lane);
         // the tokens' factors: [a][b][sv][zv] of 64, four tokens at a time
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
-        const uint32_t pages_ok = cmask[3 * ck].x;
-        const uint4 wl = cmask[3 * ck + 1], wh = cmask[3 * ck + 2];
-        const uint32_t wild0 = wl.x | wl.y | wl.z | wl.w, wild1 = wh.x | wh.y | wh.z | wh.w;
+        const uint4 odd = cmask[3 * ck];
         const int t0 = (pw.first + pw.lo + i) * C::ST;
-        const bool full = __all_sync(0xffffffffu, t0 >= lo_t && t0 + C::ST <= lim && pages_ok == 0xFu &&
-                                                      (wild0 | wild1) == 0u);
-        // scores in the operand's units (times `down`: base-2 scores), in place of S
+        // every row of the warp attends every token (the same for all its lanes)
+        const bool full = t0 >= lo_max && t0 + C::ST <= lim_min && (odd.x | odd.y | odd.z | odd.w) == 0u;
+        // Scores in the operand's units (times `down`: base-2 scores), in place of
+        // S. The stages of what follows are written out a chunk of 16 tokens ahead
+        // of one another: loads, products and exponentials of one chunk cover the
+        // latencies of the next.
         float2* x2 = reinterpret_cast<float2*>(sr);
-        const float2 qs2 = make_float2(qsum, qsum), k2 = make_float2(qk_scale, qk_scale);
+        if constexpr (C::F8 || C::ZP) {
+          const float2 qs2 = make_float2(qsum, qsum);
+          float4 fa[2][4], fb[2][C::ZP ? 4 : 1];
+          auto factors = [&](int c) {
 #pragma unroll
-        for (int k = 0; k < C::ST / 2; k += 2) {
-          const float2 s0 = make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
-          const float2 s1 = make_float2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3]));
-          if constexpr (C::BF || C::SI) {
-            x2[k] = __fmul2_rn(s0, k2);
-            x2[k + 1] = __fmul2_rn(s1, k2);
-          } else {
-            const float4 a = cm4[k / 2];
-            if constexpr (C::ZP) {
-              const float4 b = cm4[C::ST / 4 + k / 2];
-              x2[k] = __ffma2_rn(s0, make_float2(a.x, a.y), __fmul2_rn(make_float2(b.x, b.y), qs2));
-              x2[k + 1] = __ffma2_rn(s1, make_float2(a.z, a.w), __fmul2_rn(make_float2(b.z, b.w), qs2));
-            } else {
-              x2[k] = __fmul2_rn(s0, make_float2(a.x, a.y));
-              x2[k + 1] = __fmul2_rn(s1, make_float2(a.z, a.w));
+            for (int j = 0; j < 4; ++j) {
+              fa[c & 1][j] = cm4[4 * c + j];
+              if constexpr (C::ZP) fb[c & 1][j] = cm4[C::ST / 4 + 4 * c + j];
+            }
+          };
+          factors(0);
+#pragma unroll
+          for (int c = 0; c < C::ST / 16; ++c) {
+            if (c + 1 < C::ST / 16) factors(c + 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int k = 8 * c + 2 * j;
+              const float4 a = fa[c & 1][j];
+              if constexpr (C::ZP) {
+                const float4 b = fb[c & 1][j];
+                x2[k] = __ffma2_rn(x2[k], make_float2(a.x, a.y), __fmul2_rn(make_float2(b.x, b.y), qs2));
+                x2[k + 1] = __ffma2_rn(x2[k + 1], make_float2(a.z, a.w), __fmul2_rn(make_float2(b.z, b.w), qs2));
+              } else {
+                x2[k] = __fmul2_rn(x2[k], make_float2(a.x, a.y));
+                x2[k + 1] = __fmul2_rn(x2[k + 1], make_float2(a.z, a.w));
+              }
             }
           }
         }
@@ -1081,6 +1118,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           // the tokens this row attends, as bits
           auto low = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; };
           uint64_t vis = low(lim - t0) & ~low(lo_t - t0);
+          const uint32_t pages_ok = cpages[ck];
+          const uint4 wl = cmask[3 * ck + 1], wh = cmask[3 * ck + 2];
+          const uint32_t wild0 = wl.x | wl.y | wl.z | wl.w, wild1 = wh.x | wh.y | wh.z | wh.w;
 #pragma unroll
           for (int pg = 0; pg < C::PPS; ++pg)
             if (((pages_ok >> pg) & 1u) == 0u) vis &= ~(0xffffull << (16 * pg));
@@ -1094,93 +1134,108 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         }
         float mt;
         {
-          float m0 = -INFINITY, m1 = -INFINITY;
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < C::ST; k += 4) {
-            m0 = max3(m0, __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
-            m1 = max3(m1, __uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3]));
-          }
-          mt = fmaxf(m0, m1) * down;
+          for (int k = 0; k < C::ST; k += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              m4[j] = max3(m4[j], __uint_as_float(sr[k + 2 * j]), __uint_as_float(sr[k + 2 * j + 1]));
+          mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * down;
         }
         if constexpr (C::F8 || C::ZP) {
           const float4 lt = cm4[C::ST];      // log2 of the largest V scales
           mt += fmaxf(lt.x, lt.y);
         }
-        const bool move = mt > m_run + 8.f;
-        const float alpha = move && m_run != -INFINITY ? ex2_ftz(m_run - mt) : 1.f;
-        m_run = move ? mt : m_run;
-        l *= alpha;
-        corr *= alpha;
-        const float mref = m_run == -INFINITY ? 0.f : m_run;
-        const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
-        if (rescale) {
-          wait_all(pvdone + x, (cnt - 1) & 1);
-          tc_fence_after();
+        bool pv_seen = false;
+        if (__any_sync(0xffffffffu, mt > m_run + 8.f)) {
+          const bool move = mt > m_run + 8.f;
+          const float alpha = move && m_run != -INFINITY ? ex2_ftz(m_run - mt) : 1.f;
+          m_run = move ? mt : m_run;
+          mref = m_run == -INFINITY ? 0.f : m_run;
+          l *= alpha;
+          corr *= alpha;
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            wait_all(pvdone + x, (cnt - 1) & 1);
+            tc_fence_after();
+            pv_seen = true;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t ov[16];
-            tmem_ld16(t_o + 16 * c, ov);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t ov[16];
+              tmem_ld16(t_o + 16 * c, ov);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st16(t_o + 16 * c, ov);
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st16(t_o + 16 * c, ov);
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
         }
-        // weights, 32 tokens at a time, as pairs of 16-bit values
+        // weights 2^(x down - m), as pairs of 16-bit values
         const float2 dn2 = make_float2(down, down), nm2 = make_float2(-mref, -mref);
-        float2 ls2 = make_float2(0.f, 0.f), cz2 = make_float2(0.f, 0.f);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, cz2 = make_float2(0.f, 0.f);
+        constexpr int NCH = C::ST / 16;
+        auto expo = [&](int c) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
-          float4 sv4 = make_float4(1.f, 1.f, 1.f, 1.f), zv4 = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = __ffma2_rn(x2[k], dn2, nm2);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int kk = 16 * hf + k;
-            if constexpr (C::F8 || C::ZP) {
-              if ((k & 1) == 0) sv4 = cm4[C::ST / 2 + kk / 2];
+          for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = make_float2(ex2_ftz(x2[k].x), ex2_ftz(x2[k].y));
+        };
+        uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
+        float4 fs[4], fz[C::ZP ? 4 : 1];
+        expo(0);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          if constexpr (C::F8 || C::ZP) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              fs[j] = cm4[C::ST / 2 + 4 * c + j];
+              if constexpr (C::ZP) fz[j] = cm4[3 * C::ST / 4 + 4 * c + j];
             }
-            if constexpr (C::ZP) {
-              if ((k & 1) == 0) zv4 = cm4[3 * C::ST / 4 + kk / 2];
-            }
-            const float2 e = __ffma2_rn(x2[kk], dn2, nm2);
-            const float2 p2 = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
-            ls2 = __fadd2_rn(ls2, p2);
+          }
+          if (c + 1 < NCH) expo(c + 1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int kk = 8 * c + k, o = 8 * (c & 1) + k;
+            const float2 p2 = x2[kk];
+            ls[k & 1] = __fadd2_rn(ls[k & 1], p2);
             float2 wv = p2;
             if constexpr (C::F8 || C::ZP)
-              wv = __fmul2_rn(p2, (k & 1) ? make_float2(sv4.z, sv4.w) : make_float2(sv4.x, sv4.y));
+              wv = __fmul2_rn(p2, (k & 1) ? make_float2(fs[k / 2].z, fs[k / 2].w) : make_float2(fs[k / 2].x, fs[k / 2].y));
             float2 hv;
             if constexpr (C::BF) {
               const __nv_bfloat162 b16 = __floats2bfloat162_rn(wv.x, wv.y);
-              ph[k] = *reinterpret_cast<const uint32_t*>(&b16);
-              hv = make_float2(bf16_lo(ph[k]), bf16_hi(ph[k]));
+              ph[o] = *reinterpret_cast<const uint32_t*>(&b16);
+              if constexpr (C::PP == 2) hv = make_float2(bf16_lo(ph[o]), bf16_hi(ph[o]));
             } else {
               const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
-              ph[k] = *reinterpret_cast<const uint32_t*>(&f16);
-              hv = __half22float2(f16);
+              ph[o] = *reinterpret_cast<const uint32_t*>(&f16);
+              if constexpr (C::PP == 2 || C::ZP) hv = __half22float2(f16);
             }
             if constexpr (C::PP == 2) {
               const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
               if constexpr (C::BF) {
                 const __nv_bfloat162 b16 = __floats2bfloat162_rn(rest.x, rest.y);
-                pl[k] = *reinterpret_cast<const uint32_t*>(&b16);
+                pl[o] = *reinterpret_cast<const uint32_t*>(&b16);
               } else {
                 const __half2 f16 = __floats2half2_rn(rest.x, rest.y);
-                pl[k] = *reinterpret_cast<const uint32_t*>(&f16);
+                pl[o] = *reinterpret_cast<const uint32_t*>(&f16);
                 if constexpr (C::ZP) hv = __fadd2_rn(hv, __half22float2(f16));
               }
             }
             if constexpr (C::ZP)
-              cz2 = __ffma2_rn(hv, (k & 1) ? make_float2(zv4.z, zv4.w) : make_float2(zv4.x, zv4.y), cz2);
+              cz2 = __ffma2_rn(hv, (k & 1) ? make_float2(fz[k / 2].z, fz[k / 2].w) : make_float2(fz[k / 2].x, fz[k / 2].y), cz2);
           }
-          // the last product has read P
-          if (hf == 0 && cnt > 0 && !rescale) {
-            wait_all(pvdone + x, (cnt - 1) & 1);
-            tc_fence_after();
+          if (c & 1) {
+            // the last product has read P
+            if (c == 1 && cnt > 0 && !pv_seen) {
+              wait_all(pvdone + x, (cnt - 1) & 1);
+              tc_fence_after();
+            }
+            tmem_st16(t_p + 8 * (c - 1), ph);
+            if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
           }
-          tmem_st16(t_p + 16 * hf, ph);
-          if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 16 * hf, pl);
         }
+        const float2 ls2 = __fadd2_rn(ls[0], ls[1]);
         l += ls2.x + ls2.y;
         corr += cz2.x + cz2.y;
         if (wild) l = __int_as_float(0x7fc00000);
