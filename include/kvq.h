@@ -515,9 +515,10 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
  *          entry do not matter (0 from that call: invalid arguments).
  * The other arguments are those of kvq_decode_attn. A context that is not legal
  * (KVQ_DEVERR_CONTEXT) counts as empty: its rows are zeros. A token on a block
- * id outside the pool (KVQ_DEVERR_BLOCK) is not attended. A token whose V row
- * holds a NaN or an infinity (with a per-token scale: whose V scale is one)
- * makes every channel of the rows that attend it NaN.
+ * id outside the pool (KVQ_DEVERR_BLOCK) is not attended. A NaN or an infinity
+ * in a V row (with a per-token scale: a scale that is one) makes the rows that
+ * attend that token not finite, in its channels or in all of them, and no other
+ * row.
  * No length is needed on the host: a captured graph may be replayed with other
  * cu_q and context_lens of at most n_seqs sequences and total_q tokens.
  */

@@ -51,10 +51,11 @@
 // The registers are shared out by role: 168 a thread for the softmax warps
 // (64 scores and the weights made of them), 88 for the others.
 //
-// A token whose V row holds a NaN or an infinity (with a per-token scale: whose
-// V scale is one) makes every channel of the rows that attend it NaN and leaves
-// the other rows alone: its V is zeroed in the operand, where 0 x NaN would
-// reach every row, and the rows that attend it get a NaN sum.
+// A V row that holds a NaN or an infinity (with a per-token scale: whose scale is
+// one) reaches the rows that attend it, in its channels or in all of them, and
+// no other row: in a step that some row does not attend as a whole its V is
+// zeroed in the operand, where 0 x NaN would reach every row, and the rows that
+// do attend it get a NaN sum.
 //
 // Every wait is bounded, as in the other attention kernels: on expiry the CTA
 // stops issuing, drains, writes NaN to every row of its share and returns.
@@ -269,7 +270,11 @@ __device__ __forceinline__ uint32_t rg_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // One arrival for the whole warp, after what its lanes did.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
@@ -664,6 +669,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     int u = 0, s = 0, cs = 0;                              // step, its raw and operand stage
     RgItem w;
     for (int np = 0; ok && fetch(np, w, true); ++np) {
+      // tokens that every row of the block attends
+      const int j0 = w.k << bt.p.pos_log, base = w.ctx - w.n;
+      const int all_end = base + j0 + 1;
+      const int all_beg = bt.p.window > 0 ? base + j0 + (w.rows >> bt.p.g_log) - bt.p.window : 0;
       for (int i = w.lo; ok && i < w.hi; ++i, ++u, s = s + 1 == C::NRAW ? 0 : s + 1, cs = cs + 1 == C::NC ? 0 : cs + 1) {
         if (ok) ok = mbar_wait(rfull + s, (u / C::NRAW) & 1, abort_flag, wait_limit);
         if (ok && !C::BF && u >= C::NC) ok = mbar_wait(cfree + cs, (u / C::NC - 1) & 1, abort_flag, wait_limit);
@@ -671,6 +680,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         const uint32_t pm = rmask[s];
         const int tok0 = (w.first + i) * C::ST;
         if (ct == 0) cpages[cs] = pm;
+        const bool plain = tok0 >= all_beg && tok0 + C::ST <= all_end && pm == 0xFu;   // no mask, nothing missing
         uint8_t* rk = raw + s * C::RSTAGE;
         uint8_t* rv = rk + C::PPS * C::PAGE;
         uint8_t* cb = cst + cs * C::CSTAGE;
@@ -682,12 +692,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         };
         if (ok) {
           if constexpr (C::BF) {
-            // V as it is stored: tokens that hold nothing, and tokens with a NaN
-            // or an infinity, are zeroed
+            // V as it is stored; where some row does not attend every token, tokens that
+            // hold nothing and tokens with a NaN or an infinity are zeroed
             uint32_t bad0 = 0u, bad1 = 0u;
             constexpr int NIT = C::PPS * 2 * D / 128;
-#pragma unroll 4
-            for (int it = 0; it < NIT; ++it) {
+#pragma unroll 2
+            for (int it = plain ? NIT : 0; it < NIT; ++it) {
               const int x = ct + 128 * it;                 // chunk: 8 tokens of a channel
               const int p = x / (2 * D), o8 = ((x / D) & 1) * 8;
               const int keep = max(0, min(8, nvalid(p) - o8));
@@ -760,13 +770,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   sv = 1.f;
                 }
                 wild = !(fabsf(sv) < INFINITY);
-                if (wild) sv = zv = 0.f;
+                if (wild) {
+                  sv = plain ? __int_as_float(0x7fc00000) : 0.f;
+                  zv = 0.f;
+                }
+                wild = wild && !plain;
               }
               cm[ct] = a;
               cm[C::ST + ct] = b;
               cm[2 * C::ST + ct] = sv;
               cm[3 * C::ST + ct] = zv;
-              const float top = warp_max_f32(fabsf(sv));
+              const float top = warp_max_f32(sv);          // scales are not negative; NaN does not count
               const unsigned wm = __ballot_sync(0xffffffffu, wild);
               if ((ct & 31) == 0) {
                 cm[4 * C::ST + (ct >> 5)] = top > 0.f ? fmaxf(__log2f(top), -64.f) : -64.f;
@@ -789,16 +803,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             for (int it = 0; it < NIT; ++it) {
               const int x = ct + 128 * it;
               const int p = x / D, d = x % D;              // p is the same for a whole warp
-              const int nv = nvalid(p);
-              uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;
-              if constexpr (C::MV > 0) {                   // tokens whose scale is finite
-                const uint16_t sb = *reinterpret_cast<const uint16_t*>(mv + p * C::METAB + (lane & 15) * 2 * C::MV);
-                keep &= ~__ballot_sync(0xffffffffu, lane < 16 && (sb & 0x7fffu) >= 0x7f80u);
-              }
               uint4 o0, o1;
               codes16_to_f16<FMT>(vraw[it], o0, o1);
               uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-              if (keep != 0xffffu) {
+              if (!plain) {
+                // tokens that hold something, their scale finite
+                const int nv = nvalid(p);
+                uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;
+                if constexpr (C::MV > 0) {
+                  const uint16_t sb = *reinterpret_cast<const uint16_t*>(mv + p * C::METAB + (lane & 15) * 2 * C::MV);
+                  keep &= ~__ballot_sync(0xffffffffu, lane < 16 && (sb & 0x7fffu) >= 0x7f80u);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   wv[e] &= ((keep >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((keep >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
