@@ -9,18 +9,20 @@
 // heads that share the head, token by token) and walks the cached tokens in
 // steps of 64:
 //   S[128 x 64] = Q . K^T      Q in shared memory, K codes expanded to f16
-//   P = 2^(S a + b - m)        FP32 registers, one row a thread
-//   O[128 x D] += (P sv) . V   P sv as f16 in tensor memory, V codes as f16
-// with a, sv the token's K and V scales (INT8: the zero points add b to the
-// score and leave a correction of O). The 8-bit codes are exact in f16, the
-// query is exact in f16 after a power-of-two scaling of its row (the elements
-// below 2^-29 of the largest aside), and the products accumulate in FP32: the
-// scores are those of the dequantized cache up to FP32 rounding. A BF16 cache
-// is multiplied as it is stored. Running maximum, sum and O are FP32.
-// The weights P sv are rounded to 11 bits (BF16 cache: 8) for a BF16 output,
-// whose own rounding is to 8; for an FP32 output they are kept to 22 (16) bits
-// as two parts (HP), and with static INT8 scales, where the K scale of each
-// channel multiplies the query, the query as two f16 parts.
+//   P = 2^(S a - m + e)        FP32 registers, one row a thread
+//   O[128 x D] += P . V        P as f16 in tensor memory, V codes as f16
+// with a the token's K scale. The 8-bit codes (INT8: less the zero point) are
+// exact in f16, the query is exact in f16 after a power-of-two scaling of its
+// row (the elements below 2^-29 of the largest aside), and the products
+// accumulate in FP32: the scores are those of the dequantized cache up to FP32
+// rounding. A BF16 cache is multiplied as it is stored. Running maximum, sum and
+// O are FP32.
+// For a BF16 output (itself rounded to 8 bits) P is rounded to 11 bits (BF16
+// cache: 8), and V is expanded to code * scale 2^-e, rounded to 11 bits, 2^e the
+// power of two above the step's largest V scale: so the scales cost the softmax
+// warps nothing. For an FP32 output (HP) V is the exact codes, and P times the
+// token's scale is kept to 22 (16) bits as two parts; with static INT8 scales,
+// where the K scale of each channel multiplies the query, so is the query.
 //
 // The two halves of the CTA work on different products at the same time, so
 // that one's exponentials cover the other's matrix products: slot A and slot B
@@ -31,9 +33,8 @@
 // ones in slot B, over the same rows, and joins the two at its end.
 //
 // The online softmax moves a row's reference m only when the largest weight a
-// step could give, the largest score times the step's largest V scale, passes
-// 2^8 relative to it (O is then rescaled in tensor memory). That also keeps
-// P sv inside the range of f16.
+// step could give, the largest score times 2^e, passes 2^8 relative to it (O is
+// then rescaled in tensor memory). That also keeps P inside the range of f16.
 //
 // Work split: see kvq_ragged_plan.h. A block that lies in one CTA's share is
 // finished there; the first and the last of a share may be pieces, whose
@@ -86,7 +87,7 @@ struct RgCfg {
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
   static constexpr int NC = BF ? NRAW : 3;                       // operand stages
   static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
-  static constexpr int CMETA = 4 * ST * 4 + 16;                  // a, b, sv, zv per token; 2 log2 of max sv
+  static constexpr int CMETA = 2 * ST * 4 + 16;                  // a, sv per token; e, 2^-e of the step
   static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
@@ -101,8 +102,8 @@ struct RgCfg {
   static constexpr int OFF_C = OFF_Q + 2 * QBYTES;
   static constexpr int OFF_RM = (OFF_C + NC * CSTAGE + 15) / 16 * 16;
   static constexpr int OFF_X = OFF_RM + NRAW * RMETA;            // float [16][128]: joining the slots
-  static constexpr int OFF_XS = OFF_X + 16 * 128 * 4;            // float4 [128]: m, l, corr of slot B
-  static constexpr int OFF_BAR = OFF_XS + 128 * 16;
+  static constexpr int OFF_XS = OFF_X + 16 * 128 * 4;            // float2 [128]: m, l of slot B
+  static constexpr int OFF_BAR = OFF_XS + 128 * 8;
   static constexpr int NBAR = 2 * NRAW + 2 * NC + 8 + 2 + 2 * kRgRing;
   static constexpr int OFF_MASK = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;   // page masks [NRAW], [NC], then [NC][12]
   static constexpr int OFF_RED = OFF_MASK + 16 * ((NRAW + NC + 3) / 4) + 48 * NC;
@@ -317,6 +318,35 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
   return e != 0u;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Four int8 codes less a zero point as f16 (exact): 1024 + (c + 128) by a byte
+// permute, minus z = 1152 + zero point, an integer of [1024, 1279]; z0 for codes
+// 0 and 1, z1 for 2 and 3.
+__device__ __forceinline__ void s8x4_less(uint32_t w, uint32_t z0, uint32_t z1, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = w ^ 0x80808080u;
+  const uint32_t p0 = __byte_perm(x, 0x64646464u, 0x4140), p1 = __byte_perm(x, 0x64646464u, 0x4342);
+  const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&p0), *reinterpret_cast<const __half2*>(&z0));
+  const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&p1), *reinterpret_cast<const __half2*>(&z1));
+  lo = *reinterpret_cast<const uint32_t*>(&h0);
+  hi = *reinterpret_cast<const uint32_t*>(&h1);
+}
+// 16 codes: the same zero point for all, or one for each.
+__device__ __forceinline__ void codes16_less(const uint4 c, uint32_t z, uint4& o0, uint4& o1) {
+  s8x4_less(c.x, z, z, o0.x, o0.y);
+  s8x4_less(c.y, z, z, o0.z, o0.w);
+  s8x4_less(c.z, z, z, o1.x, o1.y);
+  s8x4_less(c.w, z, z, o1.z, o1.w);
+}
+__device__ __forceinline__ void codes16_less_pairs(const uint4 c, const uint32_t* z, uint4& o0, uint4& o1) {
+  s8x4_less(c.x, z[0], z[1], o0.x, o0.y);
+  s8x4_less(c.y, z[2], z[3], o0.z, o0.w);
+  s8x4_less(c.z, z[4], z[5], o1.x, o1.y);
+  s8x4_less(c.w, z[6], z[7], o1.z, o1.w);
 }
 
 constexpr int kRgThreads = 512;
@@ -735,92 +765,111 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               cmw[8 + (ct >> 5)] = bad1;
             }
           } else {
-            const uint32_t rka = smem_u32(rk), rva = smem_u32(rv);
-            const uint32_t cka = smem_u32(cb), cva = cka + C::PPS * C::CPAGE;
+            // A warp has one page of the step. Every raw chunk is loaded before any
+            // converted one is stored.
+            const int pw = ct >> 5;
+            const uint32_t rka = smem_u32(rk) + pw * C::PAGE, rva = smem_u32(rv) + pw * C::PAGE;
+            const uint32_t cka = smem_u32(cb) + pw * C::CPAGE, cva = cka + C::PPS * C::CPAGE;
             float* cm = reinterpret_cast<float*>(cb + 2 * C::PPS * C::CPAGE);
             const uint8_t* mk = rmeta + s * C::RMETA;
             const uint8_t* mv = mk + C::PPS * C::METAB;
-            // every raw chunk is loaded before any converted one is stored
-            constexpr int NIT = C::PPS * D / 128;
+            constexpr int NIT = D / 32;
             uint4 kraw[NIT], vraw[NIT];
 #pragma unroll
-            for (int it = 0; it < NIT; ++it) {
-              const int x = ct + 128 * it;                 // K: 16 channels of a token; V: 16 tokens of a channel
-              kraw[it] = lds_u4(rka + x * 16);
-              vraw[it] = lds_u4(rva + x * 16);
+            for (int it = 0; it < NIT; ++it) {               // K: 16 channels of a token; V: 16 tokens of a channel
+              kraw[it] = lds_u4(rka + (lane + 32 * it) * 16);
+              vraw[it] = lds_u4(rva + (lane + 32 * it) * 16);
             }
-            // per-token column factors: score = S a + b qsum, weight P sv, V zero point zv
-            if (ct < C::ST) {
-              const int p = ct >> 4, tk = ct & 15;
-              float a = 0.f, b = 0.f, sv = 0.f, zv = 0.f;
-              bool wild = false;
-              if (tk < nvalid(p)) {
-                if constexpr (C::F8) {
-                  a = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + p * C::METAB + tk * 2)) * qk_scale;
-                  sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + p * C::METAB + tk * 2));
-                } else if constexpr (C::ZP) {
-                  const __nv_bfloat162 km = *reinterpret_cast<const __nv_bfloat162*>(mk + p * C::METAB + tk * 4);
-                  const __nv_bfloat162 vm = *reinterpret_cast<const __nv_bfloat162*>(mv + p * C::METAB + tk * 4);
-                  a = __low2float(km) * qk_scale;
-                  b = -__low2float(km) * __high2float(km) * qk_scale;
-                  sv = __low2float(vm);
-                  zv = __high2float(vm);
-                } else {
-                  a = qk_scale;
-                  sv = 1.f;
-                }
-                wild = !(fabsf(sv) < INFINITY);
-                if (wild) {
-                  sv = plain ? __int_as_float(0x7fc00000) : 0.f;
-                  zv = 0.f;
-                }
-                wild = wild && !plain;
+            const int nv = nvalid(pw);
+            uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;   // tokens of the page that count
+            // f16 pairs of neighbouring tokens' V factors and zero points, K zero points
+            uint32_t vf[C::MV > 0 && !HP ? 8 : 1], vz[C::ZP ? 8 : 1];
+            uint32_t kz = 0u;                                // of token `lane % 16`, twice
+            if constexpr (C::MV > 0) {
+              // 2^e above the step's largest finite V scale
+              constexpr int MB = 2 * C::MV;
+              auto scale_bits = [&](int t) -> uint32_t {     // 0 for a token that holds nothing
+                if (((pm >> (t >> 4)) & 1u) == 0u || tok0 + t >= w.ctx) return 0u;
+                return *reinterpret_cast<const uint16_t*>(mv + t * MB);
+              };
+              uint32_t b0 = scale_bits(lane), b1 = scale_bits(lane + 32);
+              b0 = (b0 & 0x7fffu) >= 0x7f80u ? 0u : b0;
+              b1 = (b1 & 0x7fffu) >= 0x7f80u ? 0u : b1;
+              const uint32_t top = __reduce_max_sync(0xffffffffu, max(b0, b1));   // scales are not negative
+              const int e = top == 0u ? 0 : min(126, int(top >> 7) - 126);
+              const float dn = __int_as_float((127 - e) << 23);
+              // this page's tokens: lane % 16
+              const int t = 16 * pw + (lane & 15);
+              const bool there = (lane & 15) < nv;
+              float a = 0.f, sv = 0.f;
+              if (there) {
+                a = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB)) * qk_scale;
+                sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB));
               }
-              cm[ct] = a;
-              cm[C::ST + ct] = b;
-              cm[2 * C::ST + ct] = sv;
-              cm[3 * C::ST + ct] = zv;
-              const float top = warp_max_f32(sv);          // scales are not negative; NaN does not count
-              const unsigned wm = __ballot_sync(0xffffffffu, wild);
-              if ((ct & 31) == 0) {
-                cm[4 * C::ST + (ct >> 5)] = top > 0.f ? fmaxf(__log2f(top), -64.f) : -64.f;
-                cmw[ct < 32 ? 4 : 9] = wm;
-                cmw[ct >> 5] = (pm ^ 0xFu) | wm;
+              const bool wild = !(sv < INFINITY);
+              const uint32_t wm = __ballot_sync(0xffffffffu, wild) & 0xffffu;
+              if (wild) sv = plain ? __int_as_float(0x7fc00000) : 0.f;
+              if (!plain) keep &= ~wm;
+              // a float of each of the 16 tokens as f16 pairs
+              auto pairs = [&](float x, uint32_t* out) {
+                const uint32_t own = __half_as_ushort(__float2half_rn(x));
+                const uint32_t two = own | (__shfl_xor_sync(0xffffffffu, own, 1) << 16);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[j] = __shfl_sync(0xffffffffu, two, 2 * j);
+              };
+              if constexpr (!HP) pairs(sv * dn, vf);
+              if constexpr (C::ZP) {
+                float zk = 0.f, zv = 0.f;
+                if (there) {
+                  zk = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB + 2));
+                  zv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB + 2));
+                }
+                pairs(1152.f + zv, vz);
+                kz = __half_as_ushort(__float2half_rn(1152.f + zk)) * 0x10001u;
               }
+              if (lane < 16) {
+                cm[t] = a;
+                if constexpr (HP) cm[C::ST + t] = sv;
+              }
+              if (lane == 0) {
+                if (pw == 0) *reinterpret_cast<float2*>(cm + 2 * C::ST) = make_float2(float(e), dn);
+                const uint32_t bad = plain ? 0u : wm;
+                cmw[4 + pw] = pw < 2 ? bad << (16 * pw) : 0u;
+                cmw[8 + pw] = pw < 2 ? 0u : bad << (16 * (pw - 2));
+                cmw[pw] = (pm ^ 0xFu) | bad;
+              }
+            } else {
+              if (lane == 0) cmw[pw] = pm ^ 0xFu;
             }
 #pragma unroll
             for (int it = 0; it < NIT; ++it) {
-              const int x = ct + 128 * it;
-              const int p = x / D, k = x % D;
+              const int k = lane + 32 * it;
               const int g = k / (D / 2), rem = k % (D / 2), c = rem >> 3, tt = rem & 7;
               uint4 o0, o1;
-              codes16_to_f16<FMT>(kraw[it], o0, o1);
-              const uint32_t dst = cka + p * C::CPAGE + g * 16 * D + (2 * c) * 128 + tt * 16;
+              if constexpr (C::ZP) codes16_less(kraw[it], __shfl_sync(0xffffffffu, kz, 8 * g + tt), o0, o1);
+              else codes16_to_f16<FMT>(kraw[it], o0, o1);
+              const uint32_t dst = cka + g * 16 * D + (2 * c) * 128 + tt * 16;
               sts_u4(dst, o0.x, o0.y, o0.z, o0.w);
               sts_u4(dst + 128, o1.x, o1.y, o1.z, o1.w);
             }
 #pragma unroll
             for (int it = 0; it < NIT; ++it) {
-              const int x = ct + 128 * it;
-              const int p = x / D, d = x % D;              // p is the same for a whole warp
+              const int d = lane + 32 * it;
               uint4 o0, o1;
-              codes16_to_f16<FMT>(vraw[it], o0, o1);
+              if constexpr (C::ZP) codes16_less_pairs(vraw[it], vz, o0, o1);
+              else codes16_to_f16<FMT>(vraw[it], o0, o1);
               uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-              if (!plain) {
-                // tokens that hold something, their scale finite
-                const int nv = nvalid(p);
-                uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;
-                if constexpr (C::MV > 0) {
-                  const uint16_t sb = *reinterpret_cast<const uint16_t*>(mv + p * C::METAB + (lane & 15) * 2 * C::MV);
-                  keep &= ~__ballot_sync(0xffffffffu, lane < 16 && (sb & 0x7fffu) >= 0x7f80u);
-                }
+              if constexpr (C::MV > 0 && !HP) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  wv[e] &= ((keep >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((keep >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+                for (int j = 0; j < 8; ++j) wv[j] = mul_f16x2(wv[j], vf[j]);
               }
-              const uint32_t pg = cva + p * C::CPAGE;
-              sts_u4(pg + d * 16, wv[0], wv[1], wv[2], wv[3]);
-              sts_u4(pg + (D + d) * 16, wv[4], wv[5], wv[6], wv[7]);
+              if (!plain) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  wv[j] &= ((keep >> (2 * j)) & 1u ? 0x0000FFFFu : 0u) | ((keep >> (2 * j + 1)) & 1u ? 0xFFFF0000u : 0u);
+              }
+              sts_u4(cva + d * 16, wv[0], wv[1], wv[2], wv[3]);
+              sts_u4(cva + (D + d) * 16, wv[4], wv[5], wv[6], wv[7]);
             }
           }
           fence_proxy_async_smem();
@@ -842,7 +891,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     const uint32_t t_s = tmem + lane_base + C::COL_S + x * 64;
     const uint32_t t_p = tmem + lane_base + C::COL_P + x * 64;
     float* xch = reinterpret_cast<float*>(smem + C::OFF_X);              // [16][128]
-    float4* xsum = reinterpret_cast<float4*>(smem + C::OFF_XS);          // [128]
+    float2* xsum = reinterpret_cast<float2*>(smem + C::OFF_XS);          // [128]
     const int pair_bar = 2 + quarter;                      // the two warps of this lane quarter
     const int gshift = bt.p.g_log, G = 1 << gshift;
     bool ok = true;
@@ -859,12 +908,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     // 16-byte chunks). A warp takes its 32 rows eight at a time, a lane one row
     // (lane % 8) of them and every fourth chunk: 64 contiguous bytes a row from
     // global memory, 512 to shared memory. `down` takes the scores of this thread's own
-    // row (lane = 8 (lane / 8) + lane % 8) back to the row's units, qsum is the
-    // sum of its operand's values (the zero-point term). With one block of rows
-    // for both slots, slot A's warps write it.
-    auto store_q = [&](const RgItem& w, float& down, float& qsum) {
+    // row (lane = 8 (lane / 8) + lane % 8) back to the row's units. With one block
+    // of rows for both slots, slot A's warps write it.
+    auto store_q = [&](const RgItem& w, float& down) {
       down = 1.f;
-      qsum = 0.f;
       const bool two = w.rows > 128;
       const int rs = lane & 7, cs = lane >> 3;
       const bool wr = two || x == 0;
@@ -946,7 +993,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             up = copysignf(up, qk_scale);
             if (rg == cs) down *= fabsf(qk_scale);
           }
-          float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             uint32_t hi[4], lo[4];
@@ -960,7 +1006,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                 const __half2 l2 = __floats2half2_rn(a - __low2float(h2), b - __high2float(h2));
                 lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
               }
-              if constexpr (C::ZP) sum += __low2float(h2) + __high2float(h2);
             }
             if (wr) {
               *reinterpret_cast<uint4*>(dst + rg * C::Q_SBO + 4 * i * C::Q_LBO) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -968,11 +1013,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                 *reinterpret_cast<uint4*>(dst + C::QBYTES + rg * C::Q_SBO + 4 * i * C::Q_LBO) =
                     make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-          }
-          if constexpr (C::ZP) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            if (rg == cs) qsum = sum;
           }
         }
       }
@@ -1036,9 +1076,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 
     RgItem pw;
     bool more = next_item(pw);
-    float down = 1.f, qsum = 0.f;
+    float down = 1.f;
     if (more) {
-      store_q(pw, down, qsum);
+      store_q(pw, down);
       warp_arrive(qready, lane);
     }
     int u0 = 0;                                            // the piece's first step
@@ -1055,7 +1095,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       const int lim = row_ok ? max(0, p + 1) : INT_MAX;
       const int lo_t = row_ok && bt.p.window > 0 ? max(0, p + 1 - bt.p.window) : 0;
       const int lim_min = __reduce_min_sync(0xffffffffu, lim), lo_max = __reduce_max_sync(0xffffffffu, lo_t);
-      float m_run = -INFINITY, mref = 0.f, l = 0.f, corr = 0.f;   // mref: m_run, or 0 where it is -inf
+      float m_run = -INFINITY, mref = 0.f, l = 0.f;   // mref: m_run, or 0 where it is -inf
       bool any_step = false;
       // operand stage, and its phase, of this slot's first step
       int stage = (two ? u0 : u0 + x) % C::NC;
@@ -1088,7 +1128,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        // the tokens' factors: [a][b][sv][zv] of 64, four tokens at a time
+        // the tokens' factors: [a][sv] of 64, four tokens at a time, and {e, 2^-e}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const uint4 odd = cmask[3 * ck];
         const int t0 = (pw.first + pw.lo + i) * C::ST;
@@ -1100,31 +1140,21 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         // latencies of the next.
         float2* x2 = reinterpret_cast<float2*>(sr);
         if constexpr (C::F8 || C::ZP) {
-          const float2 qs2 = make_float2(qsum, qsum);
-          float4 fa[2][4], fb[2][C::ZP ? 4 : 1];
-          auto factors = [&](int c) {
+          float4 fa[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              fa[c & 1][j] = cm4[4 * c + j];
-              if constexpr (C::ZP) fb[c & 1][j] = cm4[C::ST / 4 + 4 * c + j];
-            }
-          };
-          factors(0);
+          for (int j = 0; j < 4; ++j) fa[0][j] = cm4[j];
 #pragma unroll
           for (int c = 0; c < C::ST / 16; ++c) {
-            if (c + 1 < C::ST / 16) factors(c + 1);
+            if (c + 1 < C::ST / 16) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) fa[(c + 1) & 1][j] = cm4[4 * (c + 1) + j];
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int k = 8 * c + 2 * j;
               const float4 a = fa[c & 1][j];
-              if constexpr (C::ZP) {
-                const float4 b = fb[c & 1][j];
-                x2[k] = __ffma2_rn(x2[k], make_float2(a.x, a.y), __fmul2_rn(make_float2(b.x, b.y), qs2));
-                x2[k + 1] = __ffma2_rn(x2[k + 1], make_float2(a.z, a.w), __fmul2_rn(make_float2(b.z, b.w), qs2));
-              } else {
-                x2[k] = __fmul2_rn(x2[k], make_float2(a.x, a.y));
-                x2[k + 1] = __fmul2_rn(x2[k + 1], make_float2(a.z, a.w));
-              }
+              x2[k] = __fmul2_rn(x2[k], make_float2(a.x, a.y));
+              x2[k + 1] = __fmul2_rn(x2[k + 1], make_float2(a.z, a.w));
             }
           }
         }
@@ -1157,9 +1187,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               m4[j] = max3(m4[j], __uint_as_float(sr[k + 2 * j]), __uint_as_float(sr[k + 2 * j + 1]));
           mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * down;
         }
+        float2 ee = make_float2(0.f, 1.f);                 // e, 2^-e
         if constexpr (C::F8 || C::ZP) {
-          const float4 lt = cm4[C::ST];      // log2 of the largest V scales
-          mt += fmaxf(lt.x, lt.y);
+          ee = *reinterpret_cast<const float2*>(cm4 + C::ST / 2);
+          mt += ee.x;
         }
         bool pv_seen = false;
         if (__any_sync(0xffffffffu, mt > m_run + 8.f)) {
@@ -1168,7 +1199,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           m_run = move ? mt : m_run;
           mref = m_run == -INFINITY ? 0.f : m_run;
           l *= alpha;
-          corr *= alpha;
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
             wait_all(pvdone + x, (cnt - 1) & 1);
             tc_fence_after();
@@ -1185,9 +1215,11 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             tmem_st_wait();
           }
         }
-        // weights 2^(x down - m), as pairs of 16-bit values
-        const float2 dn2 = make_float2(down, down), nm2 = make_float2(-mref, -mref);
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, cz2 = make_float2(0.f, 0.f);
+        // weights 2^(x down - m + e), as pairs of 16-bit values (HP: 2^(x down - m), times
+        // the token's scale)
+        const float mx = HP ? -mref : ee.x - mref;
+        const float2 dn2 = make_float2(down, down), nm2 = make_float2(mx, mx);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         constexpr int NCH = C::ST / 16;
         auto expo = [&](int c) {
 #pragma unroll
@@ -1196,16 +1228,13 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = make_float2(ex2_ftz(x2[k].x), ex2_ftz(x2[k].y));
         };
         uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
-        float4 fs[4], fz[C::ZP ? 4 : 1];
+        float4 fs[4];
         expo(0);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
-          if constexpr (C::F8 || C::ZP) {
+          if constexpr (HP && (C::F8 || C::ZP)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              fs[j] = cm4[C::ST / 2 + 4 * c + j];
-              if constexpr (C::ZP) fz[j] = cm4[3 * C::ST / 4 + 4 * c + j];
-            }
+            for (int j = 0; j < 4; ++j) fs[j] = cm4[C::ST / 4 + 4 * c + j];
           }
           if (c + 1 < NCH) expo(c + 1);
 #pragma unroll
@@ -1214,7 +1243,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             const float2 p2 = x2[kk];
             ls[k & 1] = __fadd2_rn(ls[k & 1], p2);
             float2 wv = p2;
-            if constexpr (C::F8 || C::ZP)
+            if constexpr (HP && (C::F8 || C::ZP))
               wv = __fmul2_rn(p2, (k & 1) ? make_float2(fs[k / 2].z, fs[k / 2].w) : make_float2(fs[k / 2].x, fs[k / 2].y));
             float2 hv;
             if constexpr (C::BF) {
@@ -1224,7 +1253,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             } else {
               const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
               ph[o] = *reinterpret_cast<const uint32_t*>(&f16);
-              if constexpr (C::PP == 2 || C::ZP) hv = __half22float2(f16);
+              if constexpr (C::PP == 2) hv = __half22float2(f16);
             }
             if constexpr (C::PP == 2) {
               const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
@@ -1234,11 +1263,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               } else {
                 const __half2 f16 = __floats2half2_rn(rest.x, rest.y);
                 pl[o] = *reinterpret_cast<const uint32_t*>(&f16);
-                if constexpr (C::ZP) hv = __fadd2_rn(hv, __half22float2(f16));
               }
             }
-            if constexpr (C::ZP)
-              cz2 = __ffma2_rn(hv, (k & 1) ? make_float2(fz[k / 2].z, fz[k / 2].w) : make_float2(fz[k / 2].x, fz[k / 2].y), cz2);
           }
           if (c & 1) {
             // the last product has read P
@@ -1251,8 +1277,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           }
         }
         const float2 ls2 = __fadd2_rn(ls[0], ls[1]);
-        l += ls2.x + ls2.y;
-        corr += cz2.x + cz2.y;
+        l += HP ? ls2.x + ls2.y : (ls2.x + ls2.y) * ee.y;
         if (wild) l = __int_as_float(0x7fc00000);
         tmem_st_wait();
         tc_fence_before();
@@ -1267,10 +1292,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // the next piece's query, once the products that read this one's have completed
       RgItem nxt;
       const bool more_n = next_item(nxt);
-      float down_n = 1.f, qsum_n = 0.f;
+      float down_n = 1.f;
       if (more_n) {
         if (!two && x == 0 && nsteps > 1) wait_all(sfull + 1, (cnt_other - 1) & 1);
-        store_q(nxt, down_n, qsum_n);
+        store_q(nxt, down_n);
         warp_arrive(qready, lane);
       }
 
@@ -1279,16 +1304,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       tc_fence_after();
       float ma = 1.f, mb = 0.f;                            // O = ma O_A + mb O_B (one block of rows)
       if (!two && active) {
-        if (x == 1) xsum[r] = any_step ? make_float4(m_run, l, corr, 0.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (x == 1) xsum[r] = any_step ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
         named_bar_sync(pair_bar, 64);
         if (x == 0) {
-          const float4 o = xsum[r];
+          const float2 o = xsum[r];
           const float m = fmaxf(m_run, o.x);
           const float mr = m == -INFINITY ? 0.f : m;
           ma = ex2_ftz(m_run - mr);
           mb = ex2_ftz(o.x - mr);
           l = l * ma + o.y * mb;
-          corr = corr * ma + o.z * mb;
           m_run = m;
         }
       }
@@ -1321,7 +1345,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           if (row_ok && (two || x == 0)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float y = o[e] - corr;
+              float y = o[e];
               if constexpr (C::SI) y *= __bfloat162float(vs[per_tensor ? 0 : pw.h * D + 16 * c + e]);
               o[e] = y * inv;
             }
@@ -1342,7 +1366,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tc_fence_before();
       }
       down = down_n;
-      qsum = qsum_n;
       pw = nxt;
       more = more_n;
     }
