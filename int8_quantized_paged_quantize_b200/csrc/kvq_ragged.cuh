@@ -9,20 +9,24 @@
 // heads that share the head, token by token) and walks the cached tokens in
 // steps of 64:
 //   S[128 x 64] = Q . K^T      Q in shared memory, K codes expanded to f16
-//   P = 2^(S a - m + e)        FP32 registers, one row a thread
+//   P = 2^(S f - m)            FP32 registers, one row a thread
 //   O[128 x D] += P . V        P as f16 in tensor memory, V codes as f16
-// with a the token's K scale. The 8-bit codes (INT8: less the zero point) are
-// exact in f16, the query is exact in f16 after a power-of-two scaling of its
-// row (the elements below 2^-29 of the largest aside), and the products
-// accumulate in FP32: the scores are those of the dequantized cache up to FP32
-// rounding. A BF16 cache is multiplied as it is stored. Running maximum, sum and
-// O are FP32.
-// For a BF16 output (itself rounded to 8 bits) P is rounded to 11 bits (BF16
-// cache: 8), and V is expanded to code * scale 2^-e, rounded to 11 bits, 2^e the
-// power of two above the step's largest V scale: so the scales cost the softmax
-// warps nothing. For an FP32 output (HP) V is the exact codes, and P times the
-// token's scale is kept to 22 (16) bits as two parts; with static INT8 scales,
-// where the K scale of each channel multiplies the query, so is the query.
+// The 8-bit codes (INT8: less the zero point) are exact in f16, the query is
+// exact in f16 after a power-of-two scaling of its row (the elements below
+// 2^-29 of the largest aside), and the products accumulate in FP32. A BF16 cache
+// is multiplied as it is stored. Running maximum, sum and O are FP32.
+// The scales of the tokens, two ways:
+//   BF16 output: K and V are expanded to code * scale 2^-e (e of the step and of
+//     K or V: 2^e the power of two above the largest scale), rounded to 11 bits;
+//     f = 2^eK sm_scale, and P takes 2^eV. P is rounded to 11 bits (BF16 cache:
+//     8). The output itself is rounded to 8. The softmax warps see no scale of a
+//     token: its 64 factors a step and thread, from shared memory, cost them as
+//     much as half of the exponentials.
+//   FP32 output (HP): the codes stay as they are, the scores take the token's K
+//     scale in FP32 and so are those of the dequantized cache, P times the
+//     token's V scale is kept to 22 (16) bits as two parts.
+// With static INT8 scales the K scale of each channel multiplies the query (HP:
+// kept as two f16 parts) and the V scale the finished channel.
 //
 // The two halves of the CTA work on different products at the same time, so
 // that one's exponentials cover the other's matrix products: slot A and slot B
@@ -33,7 +37,7 @@
 // ones in slot B, over the same rows, and joins the two at its end.
 //
 // The online softmax moves a row's reference m only when the largest weight a
-// step could give, the largest score times 2^e, passes 2^8 relative to it (O is
+// step could give, the largest score times 2^eV, passes 2^8 relative to it (O is
 // then rescaled in tensor memory). That also keeps P inside the range of f16.
 //
 // Work split: see kvq_ragged_plan.h. A block that lies in one CTA's share is
@@ -87,7 +91,8 @@ struct RgCfg {
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
   static constexpr int NC = BF ? NRAW : 3;                       // operand stages
   static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
-  static constexpr int CMETA = 2 * ST * 4 + 16;                  // a, sv per token; e, 2^-e of the step
+  static constexpr bool COLS = HP && MV > 0;                     // scores scaled token by token
+  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K, V scale per token; eV, 2^-eV, 2^eK of the step
   static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
@@ -782,28 +787,33 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             }
             const int nv = nvalid(pw);
             uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;   // tokens of the page that count
-            // f16 pairs of neighbouring tokens' V factors and zero points, K zero points
+            // f16 pairs of neighbouring tokens' V factors and zero points; K factor and
+            // zero point of token `lane % 16`, twice
             uint32_t vf[C::MV > 0 && !HP ? 8 : 1], vz[C::ZP ? 8 : 1];
-            uint32_t kz = 0u;                                // of token `lane % 16`, twice
+            uint32_t kf = 0u, kz = 0u;
             if constexpr (C::MV > 0) {
-              // 2^e above the step's largest finite V scale
+              // 2^e above the step's largest finite scale
               constexpr int MB = 2 * C::MV;
-              auto scale_bits = [&](int t) -> uint32_t {     // 0 for a token that holds nothing
-                if (((pm >> (t >> 4)) & 1u) == 0u || tok0 + t >= w.ctx) return 0u;
-                return *reinterpret_cast<const uint16_t*>(mv + t * MB);
+              auto top_of = [&](const uint8_t* m) -> int {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int t = lane + 32 * z;
+                  uint32_t v = 0u;                           // for a token that holds nothing
+                  if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(m + t * MB);
+                  if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);   // scales are not negative
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                return top == 0u ? 0 : min(126, int(top >> 7) - 126);
               };
-              uint32_t b0 = scale_bits(lane), b1 = scale_bits(lane + 32);
-              b0 = (b0 & 0x7fffu) >= 0x7f80u ? 0u : b0;
-              b1 = (b1 & 0x7fffu) >= 0x7f80u ? 0u : b1;
-              const uint32_t top = __reduce_max_sync(0xffffffffu, max(b0, b1));   // scales are not negative
-              const int e = top == 0u ? 0 : min(126, int(top >> 7) - 126);
-              const float dn = __int_as_float((127 - e) << 23);
+              const int ev = top_of(mv), ek = HP ? 0 : top_of(mk);
+              const float vdn = __int_as_float((127 - ev) << 23), kdn = __int_as_float((127 - ek) << 23);
               // this page's tokens: lane % 16
               const int t = 16 * pw + (lane & 15);
               const bool there = (lane & 15) < nv;
-              float a = 0.f, sv = 0.f;
+              float sk = 0.f, sv = 0.f;
               if (there) {
-                a = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB)) * qk_scale;
+                sk = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB));
                 sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB));
               }
               const bool wild = !(sv < INFINITY);
@@ -811,13 +821,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               if (wild) sv = plain ? __int_as_float(0x7fc00000) : 0.f;
               if (!plain) keep &= ~wm;
               // a float of each of the 16 tokens as f16 pairs
+              auto half_bits = [](float x) -> uint32_t { return __half_as_ushort(__float2half_rn(x)); };
               auto pairs = [&](float x, uint32_t* out) {
-                const uint32_t own = __half_as_ushort(__float2half_rn(x));
+                const uint32_t own = half_bits(x);
                 const uint32_t two = own | (__shfl_xor_sync(0xffffffffu, own, 1) << 16);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) out[j] = __shfl_sync(0xffffffffu, two, 2 * j);
               };
-              if constexpr (!HP) pairs(sv * dn, vf);
+              if constexpr (!HP) {
+                pairs(sv * vdn, vf);
+                kf = half_bits(sk < INFINITY ? sk * kdn : __int_as_float(0x7fc00000)) * 0x10001u;
+              }
               if constexpr (C::ZP) {
                 float zk = 0.f, zv = 0.f;
                 if (there) {
@@ -825,14 +839,18 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   zv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB + 2));
                 }
                 pairs(1152.f + zv, vz);
-                kz = __half_as_ushort(__float2half_rn(1152.f + zk)) * 0x10001u;
+                kz = half_bits(1152.f + zk) * 0x10001u;
               }
-              if (lane < 16) {
-                cm[t] = a;
-                if constexpr (HP) cm[C::ST + t] = sv;
+              if constexpr (C::COLS) {
+                if (lane < 16) {
+                  cm[t] = sk * qk_scale;
+                  cm[C::ST + t] = sv;
+                }
               }
               if (lane == 0) {
-                if (pw == 0) *reinterpret_cast<float2*>(cm + 2 * C::ST) = make_float2(float(e), dn);
+                if (pw == 0)
+                  *reinterpret_cast<float4*>(cm + (C::COLS ? 2 * C::ST : 0)) =
+                      make_float4(float(ev), vdn, __int_as_float((127 + ek) << 23), 0.f);
                 const uint32_t bad = plain ? 0u : wm;
                 cmw[4 + pw] = pw < 2 ? bad << (16 * pw) : 0u;
                 cmw[8 + pw] = pw < 2 ? 0u : bad << (16 * (pw - 2));
@@ -848,6 +866,11 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               uint4 o0, o1;
               if constexpr (C::ZP) codes16_less(kraw[it], __shfl_sync(0xffffffffu, kz, 8 * g + tt), o0, o1);
               else codes16_to_f16<FMT>(kraw[it], o0, o1);
+              if constexpr (C::MV > 0 && !HP) {
+                const uint32_t f = __shfl_sync(0xffffffffu, kf, 8 * g + tt);
+                o0 = make_uint4(mul_f16x2(o0.x, f), mul_f16x2(o0.y, f), mul_f16x2(o0.z, f), mul_f16x2(o0.w, f));
+                o1 = make_uint4(mul_f16x2(o1.x, f), mul_f16x2(o1.y, f), mul_f16x2(o1.z, f), mul_f16x2(o1.w, f));
+              }
               const uint32_t dst = cka + g * 16 * D + (2 * c) * 128 + tt * 16;
               sts_u4(dst, o0.x, o0.y, o0.z, o0.w);
               sts_u4(dst + 128, o1.x, o1.y, o1.z, o1.w);
@@ -927,7 +950,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         for (int i = 0; i < NI; ++i) c[rg][i] = have ? src[4 * i] : make_uint4(0, 0, 0, 0);
       }
       uint8_t* dst = qop + (two ? x : 0) * C::QBYTES + quarter * 4 * C::Q_SBO + rs * 16 + cs * C::Q_LBO;
-      // without a scale per token, sm_scale is the row factor's (its sign the query's)
+      // sm_scale is the row factor's, its sign the query's (HP: the tokens' factors have it)
       if constexpr (C::BF) {
         down = fabsf(qk_scale);
         const uint32_t sg = qk_scale < 0.f ? 0x80008000u : 0u;
@@ -989,7 +1012,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           e2 = max(-100, min(100, e2));
           float up = __int_as_float((127 + e2) << 23);
           if (rg == cs) down = __int_as_float((127 - e2) << 23);
-          if constexpr (C::SI) {
+          if constexpr (!C::COLS) {
             up = copysignf(up, qk_scale);
             if (rg == cs) down *= fabsf(qk_scale);
           }
@@ -1128,18 +1151,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        // the tokens' factors: [a][sv] of 64, four tokens at a time, and {e, 2^-e}
+        // HP: the tokens' K and V scales, four at a time; then {eV, 2^-eV, 2^eK}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const uint4 odd = cmask[3 * ck];
         const int t0 = (pw.first + pw.lo + i) * C::ST;
         // every row of the warp attends every token (the same for all its lanes)
         const bool full = t0 >= lo_max && t0 + C::ST <= lim_min && (odd.x | odd.y | odd.z | odd.w) == 0u;
-        // Scores in the operand's units (times `down`: base-2 scores), in place of
-        // S. The stages of what follows are written out a chunk of 16 tokens ahead
+        // Scores in the operand's units (times f: base-2 scores), in place of S. The stages of what follows are written out a chunk of 16 tokens ahead
         // of one another: loads, products and exponentials of one chunk cover the
         // latencies of the next.
         float2* x2 = reinterpret_cast<float2*>(sr);
-        if constexpr (C::F8 || C::ZP) {
+        if constexpr (C::COLS) {
           float4 fa[2][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) fa[0][j] = cm4[j];
@@ -1177,6 +1199,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             if (!((v1 >> c) & 1u)) sr[32 + c] = 0xff800000u;
           }
         }
+        float4 ee = make_float4(0.f, 1.f, 1.f, 0.f);       // eV, 2^-eV, 2^eK
+        if constexpr (C::MV > 0) ee = cm4[C::COLS ? C::ST / 2 : 0];
+        const float f = C::COLS ? down : down * ee.z;      // takes x to the base-2 score
         float mt;
         {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1185,12 +1210,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               m4[j] = max3(m4[j], __uint_as_float(sr[k + 2 * j]), __uint_as_float(sr[k + 2 * j + 1]));
-          mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * down;
-        }
-        float2 ee = make_float2(0.f, 1.f);                 // e, 2^-e
-        if constexpr (C::F8 || C::ZP) {
-          ee = *reinterpret_cast<const float2*>(cm4 + C::ST / 2);
-          mt += ee.x;
+          mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * f + ee.x;
         }
         bool pv_seen = false;
         if (__any_sync(0xffffffffu, mt > m_run + 8.f)) {
@@ -1215,10 +1235,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             tmem_st_wait();
           }
         }
-        // weights 2^(x down - m + e), as pairs of 16-bit values (HP: 2^(x down - m), times
+        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: 2^(x f - m), times
         // the token's scale)
         const float mx = HP ? -mref : ee.x - mref;
-        const float2 dn2 = make_float2(down, down), nm2 = make_float2(mx, mx);
+        const float2 dn2 = make_float2(f, f), nm2 = make_float2(mx, mx);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         constexpr int NCH = C::ST / 16;
         auto expo = [&](int c) {
@@ -1232,7 +1252,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         expo(0);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
-          if constexpr (HP && (C::F8 || C::ZP)) {
+          if constexpr (C::COLS) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) fs[j] = cm4[C::ST / 4 + 4 * c + j];
           }
@@ -1243,7 +1263,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             const float2 p2 = x2[kk];
             ls[k & 1] = __fadd2_rn(ls[k & 1], p2);
             float2 wv = p2;
-            if constexpr (HP && (C::F8 || C::ZP))
+            if constexpr (C::COLS)
               wv = __fmul2_rn(p2, (k & 1) ? make_float2(fs[k / 2].z, fs[k / 2].w) : make_float2(fs[k / 2].x, fs[k / 2].y));
             float2 hv;
             if constexpr (C::BF) {
