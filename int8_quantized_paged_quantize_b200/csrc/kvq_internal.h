@@ -61,6 +61,10 @@ int make_plan(int32_t batch, int32_t max_ctx, int32_t partition_tokens, const kv
 // Number of SMs of the current device (148 if no device can be queried).
 int device_sm_count();
 
+// Unique id of the current CUDA context (0 if none is current or the driver
+// cannot tell): a device that was reset has another one.
+unsigned long long context_id();
+
 // Bound, in SM clock cycles, on each pipeline wait of the decode kernels
 // launched from now on (kvq_set_wait_limit; default about one second).
 long long decode_wait_limit();

@@ -100,6 +100,8 @@ int scratch_for_current_device(void** out) {
 
 }  // namespace
 
+unsigned long long kvq::context_id() { return current_context_id(); }
+
 extern "C" int kvq_decode_attn_noalloc(const void* q, int32_t batch, const void* k_cache,
                                        const void* v_cache, const void* const* scales,
                                        const int32_t* block_tables, const int32_t* context_lens,

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <type_traits>
@@ -39,18 +40,35 @@ RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   return w;
 }
 
+// Shared-memory limit of the kernel, and the check that its registers are those
+// that it shares out anew. Both cost as much as a launch, so they are done once
+// per context (a new one, after a reset, has another id).
+template <int D, int FMT, bool HP>
+cudaError_t prepare() {
+  auto kern = ragged_mma_kernel<D, FMT, HP>;
+  static std::atomic<unsigned long long> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long id = context_id();
+  if (id != 0 && dev < 64 && done[dev].load(std::memory_order_acquire) == id) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RgCfg<D, FMT, HP>::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRgRegs) return cudaErrorInvalidConfiguration;
+  if (id != 0 && dev < 64) done[dev].store(id, std::memory_order_release);
+  return cudaSuccess;
+}
+
 template <int D, int FMT, bool HP>
 cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tensor, cudaStream_t st) {
   using C = RgCfg<D, FMT, HP>;
   using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
   auto kern = ragged_mma_kernel<D, FMT, HP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = prepare<D, FMT, HP>();
   if (e != cudaSuccess) return e;
-  // the kernel shares its launch's registers out anew; it must own them all
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRgRegs) return cudaErrorInvalidConfiguration;
   const int G = d.n_q_heads / d.n_kv_heads;
   const RgSpace w = rg_space(a.total_q, d);
   char* ws = static_cast<char*>(a.workspace);

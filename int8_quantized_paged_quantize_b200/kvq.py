@@ -8,7 +8,6 @@ there is no CPU path.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -367,42 +366,64 @@ def prefill_attn(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_le
 # These calls launch on the device that holds their tensors, whichever is
 # current, and on its current stream unless one is given. What they allocate
 # themselves (an output or a workspace that is not passed) is allocated on the
-# stream that they launch on.
-def _on(dev, stream):
-    """A context in which `dev` is current and `stream` (or its own current one) too."""
-    if stream is not None and stream.device != dev:
-        raise KvqError(f"the stream is on {stream.device}, the tensors are on {dev}")
+# stream that they launch on. A decode step's calls take a few microseconds on
+# the GPU, so the checks here are kept short: pointers go to ctypes as integers,
+# and no context is entered where the device and stream are the current ones.
+_PAIR = ctypes.c_void_p * 2
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _launch_on(t, stream, name):
+    """Device index of tensor t, and the context to launch in (None: the current
+    device and stream will do)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise KvqError(f"{name} must be on a CUDA device")
     if stream is not None:
-        return torch.cuda.stream(stream)
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        if stream.device != t.device:
+            raise KvqError(f"the stream is on {stream.device}, {name} is on {t.device}")
+        return dev, torch.cuda.stream(stream)
+    return dev, None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _need_on(dev, t, dtype, name, shape=None):
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise KvqError(f"{name} must be a contiguous {dtype} tensor on {dev}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _within(ctx, fn, *args):
+    if ctx is None:
+        return fn(*args)
+    with ctx:
+        return fn(*args)
+
+
+def _at(dev, t, dtype, name, shape=None):
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise KvqError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
         raise KvqError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _need_cache(dev, k_cache, v_cache, k_scale, v_scale):
+def _cache_at(dev, k_cache, v_cache, k_scale, v_scale):
+    """Addresses of the cache arrays, and the pair of scale addresses."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise KvqError(f"{name} must be a contiguous tensor on {dev}")
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise KvqError(f"{name} must be a contiguous tensor on cuda:{dev}")
+    return (k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr() if k_scale is not None else 0,
+            v_scale.data_ptr() if v_scale is not None else 0)
 
 
-def _need_rows(dev, t, name, heads, head_dim):
-    """[T][heads][head_dim] BF16 with the heads of a token contiguous; the
-    stride between tokens in elements."""
-    if t.dtype != torch.bfloat16 or t.device != dev:
-        raise KvqError(f"{name} must be a bfloat16 tensor on {dev}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise KvqError(f"{name} must be [tokens][{heads}][{head_dim}], not {tuple(t.shape)}")
+def _rows_at(dev, t, name, tokens, heads, head_dim):
+    """Address of [tokens][heads][head_dim] BF16 with the values of a token
+    contiguous, and the elements between tokens."""
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        raise KvqError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+    if t.shape != (tokens, heads, head_dim):
+        raise KvqError(f"{name} must be [{tokens}][{heads}][{head_dim}], not {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != head_dim and heads > 1):
         raise KvqError(f"the values of a token must be contiguous in {name}")
-    return s0 if t.shape[0] > 1 else heads * head_dim
+    return t.data_ptr(), (s0 if tokens > 1 else heads * head_dim)
 
 
 def append_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
@@ -413,37 +434,35 @@ def append_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cac
     positions [T] int32; cos_sin [max_position][rotary_dim] float32 (cosines,
     then sines); slot_mapping [T] int64 (negative: not stored). q_out [T][Hq][D]
     receives the rotated query and is returned (None: allocated)."""
-    dev = k.device
-    if not k.is_cuda:
-        raise KvqError("k must be on a CUDA device")
-    T, D = k.shape[0], d.head_dim
-    ks = _need_rows(dev, k, "k", d.n_kv_heads, D)
-    vs = _need_rows(dev, v, "v", d.n_kv_heads, D)
-    if v.shape[0] != T:
-        raise KvqError("k and v must have the same number of tokens")
-    qs = 0
+    dev, ctx = _launch_on(k, stream, "k")
+    return _within(ctx, _append_rope, dev, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache,
+                   v_cache, k_scale, v_scale, fmt, d, interleaved)
+
+
+def _append_rope(dev, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale,
+                 v_scale, fmt, d, interleaved):
+    T, Hq, Hk, D = k.shape[0], d.n_q_heads, d.n_kv_heads, d.head_dim
+    kp, ks = _rows_at(dev, k, "k", T, Hk, D)
+    vp, vs = _rows_at(dev, v, "v", T, Hk, D)
+    qp = qs = qo = 0
     if q is not None:
-        qs = _need_rows(dev, q, "q", d.n_q_heads, D)
-        if q.shape[0] != T:
-            raise KvqError("q and k must have the same number of tokens")
+        qp, qs = _rows_at(dev, q, "q", T, Hq, D)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+            qo = q_out.data_ptr()
+        else:
+            qo = _at(dev, q_out, _BF16, "q_out", (T, Hq, D))
     elif q_out is not None:
         raise KvqError("q_out without q")
-    _need_on(dev, positions, torch.int32, "positions", (T,))
-    _need_on(dev, slot_mapping, torch.int64, "slot_mapping", (T,))
-    _need_on(dev, cos_sin, torch.float32, "cos_sin")
     if cos_sin.dim() != 2:
         raise KvqError("cos_sin must be [max_position][rotary_dim]")
-    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    with _on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty((T, d.n_q_heads, D), dtype=torch.bfloat16, device=dev)
-        if q_out is not None:
-            _need_on(dev, q_out, torch.bfloat16, "q_out", (T, d.n_q_heads, D))
-        _check(lib().kvq_append_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions),
-                                     _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
-                                     1 if interleaved else 0, _ptr(slot_mapping), T, _ptr(q_out),
-                                     _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                     FMT[fmt], ctypes.byref(d), _stream()), "kvq_append_rope")
+    kc, vc, ksc, vsc = _cache_at(dev, k_cache, v_cache, k_scale, v_scale)
+    rc = lib().kvq_append_rope(qp, qs, kp, ks, vp, vs, _at(dev, positions, _I32, "positions", (T,)),
+                               _at(dev, cos_sin, _F32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1],
+                               1 if interleaved else 0, _at(dev, slot_mapping, _I64, "slot_mapping", (T,)),
+                               T, qo, kc, vc, ksc, vsc, FMT[fmt], ctypes.byref(d), _raw_stream(dev))
+    if rc:
+        _check(rc, "kvq_append_rope")
     return q_out
 
 
@@ -453,35 +472,42 @@ def read(k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens, to
     k_out, v_out [total_tokens][Hk][D] (bf16 or float32) receive the tokens of
     sequence b from starts[b] on. Outputs not given are allocated; False leaves
     one out (None is returned in its place)."""
-    dev = block_tables.device
-    if not block_tables.is_cuda:
-        raise KvqError("block_tables must be on a CUDA device")
-    B = starts.numel()
-    _need_on(dev, block_tables, torch.int32, "block_tables", (B, d.max_blocks_per_seq))
-    _need_on(dev, starts, torch.int32, "starts", (B,))
-    _need_on(dev, cu_tokens, torch.int32, "cu_tokens", (B + 1,))
-    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    total = int(total_tokens)
-    shape = (total, d.n_kv_heads, d.head_dim)
-    outs = [k_out, v_out]
-    if outs[0] is False and outs[1] is False:
-        raise KvqError("nothing to read: k_out and v_out are both left out")
-    given = [t for t in outs if isinstance(t, torch.Tensor)]
-    dt = given[0].dtype if given else out_dtype
-    if dt not in (torch.bfloat16, torch.float32):
-        raise KvqError("outputs must be bfloat16 or float32")
+    dev, ctx = _launch_on(block_tables, stream, "block_tables")
+    return _within(ctx, _read, dev, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens,
+                   total_tokens, fmt, d, k_out, v_out, out_dtype)
+
+
+def _read(dev, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens, total_tokens, fmt,
+          d, k_out, v_out, out_dtype):
+    B, total = starts.numel(), int(total_tokens)
     if total < 0:
         raise KvqError("total_tokens must not be negative")
-    with _on(dev, stream):
-        outs = [None if t is False else torch.empty(shape, dtype=dt, device=dev) if t is None else t for t in outs]
-        for t, name in zip(outs, ("k_out", "v_out")):
-            if t is not None:
-                _need_on(dev, t, dt, name, shape)
-        _check(lib().kvq_read(_ptr(k_cache), _ptr(v_cache), _scales(k_scale, v_scale), _ptr(block_tables),
-                              _ptr(starts), _ptr(cu_tokens), B, total, _ptr(outs[0]), _ptr(outs[1]),
-                              0 if dt == torch.bfloat16 else 1, FMT[fmt], ctypes.byref(d), _stream()),
-               "kvq_read")
-    return outs[0], outs[1]
+    if k_out is False and v_out is False:
+        raise KvqError("nothing to read: k_out and v_out are both left out")
+    given = k_out if isinstance(k_out, torch.Tensor) else v_out
+    dt = given.dtype if isinstance(given, torch.Tensor) else out_dtype
+    if dt is not _BF16 and dt is not _F32:
+        raise KvqError("outputs must be bfloat16 or float32")
+    shape = (total, d.n_kv_heads, d.head_dim)
+    kp = vp = 0
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dt, device=block_tables.device)
+        kp = k_out.data_ptr()
+    elif k_out is not False:
+        kp = _at(dev, k_out, dt, "k_out", shape)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dt, device=block_tables.device)
+        vp = v_out.data_ptr()
+    elif v_out is not False:
+        vp = _at(dev, v_out, dt, "v_out", shape)
+    kc, vc, ks, vs = _cache_at(dev, k_cache, v_cache, k_scale, v_scale)
+    rc = lib().kvq_read(kc, vc, _PAIR(ks, vs),
+                        _at(dev, block_tables, _I32, "block_tables", (B, d.max_blocks_per_seq)),
+                        _at(dev, starts, _I32, "starts", (B,)), _at(dev, cu_tokens, _I32, "cu_tokens", (B + 1,)),
+                        B, total, kp, vp, 0 if dt is _BF16 else 1, FMT[fmt], ctypes.byref(d), _raw_stream(dev))
+    if rc:
+        _check(rc, "kvq_read")
+    return (None if k_out is False else k_out), (None if v_out is False else v_out)
 
 
 def ragged_workspace_bytes(total_q, fmt, d: Dims):
@@ -495,36 +521,42 @@ def ragged_workspace_bytes(total_q, fmt, d: Dims):
 
 def ragged_attn(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                 max_context_len, sm_scale, out, fmt: str, d: Dims, window=0, workspace=None,
-                stream=None):
+                stream=None, out_dtype=torch.bfloat16):
     """Attention of ragged chunks of new tokens over the paged cache
     (kvq_ragged_attn). q: [T][Hq][D] bf16 (a strided view will do), the new tokens
     of all sequences one after another, cu_q [B + 1] int32 where each begins; they
     are the last tokens of the sequences' contexts, already appended. out:
-    [T][Hq][D] bf16 or float32."""
-    dev = q.device
-    if not q.is_cuda:
-        raise KvqError("q must be on a CUDA device")
-    T = q.shape[0]
-    qs = _need_rows(dev, q, "q", d.n_q_heads, d.head_dim)
-    B = context_lens.numel()
-    _need_on(dev, cu_q, torch.int32, "cu_q", (B + 1,))
-    _need_on(dev, context_lens, torch.int32, "context_lens", (B,))
-    _need_on(dev, block_tables, torch.int32, "block_tables", (B, d.max_blocks_per_seq))
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    [T][Hq][D] bf16 or float32 (None: allocated, of out_dtype); returned."""
+    dev, ctx = _launch_on(q, stream, "q")
+    return _within(ctx, _ragged_attn, dev, q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                   context_lens, max_context_len, sm_scale, out, fmt, d, window, workspace, out_dtype)
+
+
+def _ragged_attn(dev, q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                 max_context_len, sm_scale, out, fmt, d, window, workspace, out_dtype):
+    T, B = q.shape[0], context_lens.numel()
+    qp, qs = _rows_at(dev, q, "q", T, d.n_q_heads, d.head_dim)
+    dt = out_dtype if out is None else out.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise KvqError("out must be bfloat16 or float32")
-    _need_on(dev, out, out.dtype, "out", tuple(q.shape))
-    _need_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = torch.empty(max(ragged_workspace_bytes(T, fmt, d), 16), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise KvqError(f"workspace must be a contiguous tensor on {dev}")
-        _check(lib().kvq_ragged_attn(_ptr(q), qs, _ptr(cu_q), B, T, _ptr(k_cache), _ptr(v_cache),
-                                     _scales(k_scale, v_scale), _ptr(block_tables), _ptr(context_lens),
-                                     int(max_context_len), int(window), float(sm_scale), _ptr(out),
-                                     _out_dtype(out), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), FMT[fmt],
-                                     ctypes.byref(d), _stream()), "kvq_ragged_attn")
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _at(dev, out, dt, "out", q.shape)
+    if workspace is None:
+        workspace = torch.empty(max(ragged_workspace_bytes(T, fmt, d), 16), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise KvqError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    kc, vc, ks, vs = _cache_at(dev, k_cache, v_cache, k_scale, v_scale)
+    rc = lib().kvq_ragged_attn(qp, qs, _at(dev, cu_q, _I32, "cu_q", (B + 1,)), B, T, kc, vc, _PAIR(ks, vs),
+                               _at(dev, block_tables, _I32, "block_tables", (B, d.max_blocks_per_seq)),
+                               _at(dev, context_lens, _I32, "context_lens", (B,)), int(max_context_len),
+                               int(window), sm_scale, op, 0 if dt is _BF16 else 1, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), FMT[fmt], ctypes.byref(d),
+                               _raw_stream(dev))
+    if rc:
+        _check(rc, "kvq_ragged_attn")
     return out
 
 
@@ -643,12 +675,9 @@ class LayerCache:
         packed, cu_q [B + 1] where each sequence's rows begin."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.dims.head_dim)
-        if out is None:
-            with _on(q.device, stream):
-                out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
         return ragged_attn(q, cu_q, self.k, self.v, self.k_scale, self.v_scale, block_tables,
                            context_lens, max_context_len, sm_scale, out, self.fmt, self.dims, window,
-                           workspace, stream)
+                           workspace, stream, out_dtype)
 
     # ---- copies in the logical layout [NB][Hk][block_size][D] (for inspection and tests)
     def k_logical(self, blocks=None):
