@@ -34,7 +34,10 @@
 // block of more than 128 rows puts its first 128 rows in slot A and the others
 // in slot B, and every step runs in both (the codes are expanded once for 256
 // rows). A block of at most 128 rows runs its even steps in slot A and its odd
-// ones in slot B, over the same rows, and joins the two at its end.
+// ones in slot B, over the same rows, and joins the two at its end. A block of at most 16
+// rows (a token or two of a sequence) has its rows in each of the four warps of a
+// slot, every warp with 16 of a step's tokens: a row's exponentials are spread
+// over four threads, and eight softmaxes join.
 //
 // The online softmax moves a row's reference m only when the largest weight a
 // step could give, the largest score times 2^eV, passes 2^8 relative to it (O is
@@ -73,6 +76,7 @@
 namespace kvq {
 
 constexpr int kRgRing = 4;                     // pieces handed ahead
+constexpr int kRgNarrow = 16;                  // rows that every warp of a slot has a copy of
 
 template <int D, int FMT, bool HP>
 struct RgCfg {
@@ -263,6 +267,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // Shared memory by its 32-bit address.
 __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   uint4 v;
@@ -923,7 +933,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       ok = __all_sync(0xffffffffu, ok);
     };
     // this thread's row of a block: the block row, its token of the sequence's new ones
-    auto block_row = [&](const RgItem& w) -> int { return w.rows > 128 ? x * 128 + r : r; };
+    auto block_row = [&](const RgItem& w) -> int {
+      return w.rows > 128 ? x * 128 + r : w.rows <= kRgNarrow ? lane : r;
+    };
     auto token_of = [&](const RgItem& w, int rr) -> int { return (w.k << bt.p.pos_log) + (rr >> gshift); };
     auto head_of = [&](const RgItem& w, int rr) -> int { return (w.h << gshift) + (rr & (G - 1)); };
 
@@ -942,7 +954,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       uint4 c[4][NI];
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg) {
-        const int rr = (two ? x * 128 : 0) + quarter * 32 + 8 * rg + rs;
+        const int rr = (two ? x * 128 : 0) + (w.rows <= kRgNarrow ? 0 : quarter * 32) + 8 * rg + rs;
         const bool have = rr < w.rows;
         const uint4* src = reinterpret_cast<const uint4*>(
             q + int64_t(w.row0 + (have ? token_of(w, rr) : 0)) * q_stride + int64_t(head_of(w, rr)) * D) + cs;
@@ -1073,8 +1085,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       }
     };
     // The next piece with steps; blocks in which no row attends anything get
-    // their zero rows here. The two warps of a lane quarter meet at barriers, so
-    // they go on together or not at all.
+    // their zero rows here. The eight warps meet at barriers, so they go on
+    // together or not at all.
     int np = 0;
     auto next_item = [&](RgItem& w) -> bool {
       while (true) {
@@ -1082,14 +1094,14 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         uint32_t both;
         asm volatile(
             "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+            "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
             : "=r"(both)
-            : "r"(uint32_t(mine)), "r"(pair_bar)
+            : "r"(uint32_t(mine))
             : "memory");
         if (both == 0u) return false;
         if (w.count > 0) return true;
         const int rr = block_row(w);
-        if (rr < w.rows && (w.rows > 128 || x == 0)) {
+        if (rr < w.rows && (w.rows > 128 || (x == 0 && (w.rows > kRgNarrow || quarter == 0)))) {
           OutT* dst = out + (int64_t(w.row0 + token_of(w, rr)) * (bt.Hk << gshift) + head_of(w, rr)) * D;
           const float z[16] = {};
           for (int c = 0; c < D / 16; ++c) store_row16(dst + 16 * c, z);
@@ -1120,56 +1132,52 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       const int lim_min = __reduce_min_sync(0xffffffffu, lim), lo_max = __reduce_max_sync(0xffffffffu, lo_t);
       float m_run = -INFINITY, mref = 0.f, l = 0.f;   // mref: m_run, or 0 where it is -inf
       bool any_step = false;
+      // A narrow block: all four warps of a slot have its rows, each for 16 of a
+      // step's tokens, as a softmax of their own (P is zero in the others' columns).
+      const bool narrow = pw.rows <= kRgNarrow;
+      if (narrow) {
+        const uint32_t z[16] = {};
+#pragma unroll
+        for (int c = 0; c < 2 * C::PP; ++c) tmem_st16(t_p + 16 * c, z);
+        tmem_st_wait();
+      }
       // operand stage, and its phase, of this slot's first step
       int stage = (two ? u0 : u0 + x) % C::NC;
       uint32_t phase = ((two ? u0 : u0 + x) / C::NC) & 1;
-      for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
-        const int ck = stage;
-        const uint32_t cpar = phase;
-        const int ahead = two ? 1 : 2;                     // to this slot's next step
-        stage += ahead;
-        if (stage >= C::NC) {
-          stage -= C::NC;
-          phase ^= 1u;
+      // One step: the scores of this warp's rows for `width` tokens (all 64, or with
+      // narrow blocks the warp's 16) to weights. Nothing moves the reference in
+      // most steps, and most have no mask.
+      auto softmax_step = [&](auto width, int i, int ck) {
+        constexpr int NT = decltype(width)::value;         // tokens of the step that are this warp's
+        const int col0 = NT == C::ST ? 0 : NT * quarter;   // the first of them
+        uint32_t sr[NT];
+        if constexpr (NT == C::ST) {
+          tmem_ld32(t_s, sr);
+          tmem_ld32(t_s + 32, sr + 32);
+        } else {
+          tmem_ld16(t_s + col0, sr);
         }
-        // both at once: they are mostly complete
-        if (!__all_sync(0xffffffffu, mbar_test_wait(sfull + x, cnt & 1) & mbar_test_wait(cfull + ck, cpar))) {
-          wait_all(sfull + x, cnt & 1);
-          wait_all(cfull + ck, cpar);
-        }
-        tc_fence_after();
-        if (!active) {
-          warp_arrive(sfree + x, lane);
-          if (cnt > 0) wait_all(pvdone + x, (cnt - 1) & 1);
-          warp_arrive(pready + x, lane);
-          ++cnt;
-          continue;
-        }
-        uint32_t sr[C::ST];
-        tmem_ld32(t_s, sr);
-        tmem_ld32(t_s + 32, sr + 32);
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
         // HP: the tokens' K and V scales, four at a time; then {eV, 2^-eV, 2^eK}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
+        const int q0 = col0 / 4;
         const uint4 odd = cmask[3 * ck];
         const int t0 = (pw.first + pw.lo + i) * C::ST;
         // every row of the warp attends every token (the same for all its lanes)
         const bool full = t0 >= lo_max && t0 + C::ST <= lim_min && (odd.x | odd.y | odd.z | odd.w) == 0u;
-        // Scores in the operand's units (times f: base-2 scores), in place of S. The stages of what follows are written out a chunk of 16 tokens ahead
-        // of one another: loads, products and exponentials of one chunk cover the
-        // latencies of the next.
+        // Scores in the operand's units (times f: base-2 scores), in place of S.
         float2* x2 = reinterpret_cast<float2*>(sr);
         if constexpr (C::COLS) {
           float4 fa[2][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) fa[0][j] = cm4[j];
+          for (int j = 0; j < 4; ++j) fa[0][j] = cm4[q0 + j];
 #pragma unroll
-          for (int c = 0; c < C::ST / 16; ++c) {
-            if (c + 1 < C::ST / 16) {
+          for (int c = 0; c < NT / 16; ++c) {
+            if (c + 1 < NT / 16) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) fa[(c + 1) & 1][j] = cm4[4 * (c + 1) + j];
+              for (int j = 0; j < 4; ++j) fa[(c + 1) & 1][j] = cm4[q0 + 4 * (c + 1) + j];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1191,13 +1199,16 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 #pragma unroll
           for (int pg = 0; pg < C::PPS; ++pg)
             if (((pages_ok >> pg) & 1u) == 0u) vis &= ~(0xffffull << (16 * pg));
-          const uint32_t v0 = uint32_t(vis), v1 = uint32_t(vis >> 32);
-          wild = ((v0 & wild0) | (v1 & wild1)) != 0u;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!((v0 >> c) & 1u)) sr[c] = 0xff800000u;
-            if (!((v1 >> c) & 1u)) sr[32 + c] = 0xff800000u;
+          uint64_t bad = uint64_t(wild0) | (uint64_t(wild1) << 32);
+          if constexpr (NT < C::ST) {
+            vis = (vis >> col0) & 0xffffull;
+            bad >>= col0;
           }
+          wild = (vis & bad) != 0ull;
+          const uint32_t v0 = uint32_t(vis), v1 = uint32_t(vis >> 32);
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            if (!(((c < 32 ? v0 : v1) >> (c & 31)) & 1u)) sr[c] = 0xff800000u;
         }
         float4 ee = make_float4(0.f, 1.f, 1.f, 0.f);       // eV, 2^-eV, 2^eK
         if constexpr (C::MV > 0) ee = cm4[C::COLS ? C::ST / 2 : 0];
@@ -1206,7 +1217,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < C::ST; k += 8)
+          for (int k = 0; k < NT; k += 8)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               m4[j] = max3(m4[j], __uint_as_float(sr[k + 2 * j]), __uint_as_float(sr[k + 2 * j + 1]));
@@ -1240,21 +1251,21 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         const float mx = HP ? -mref : ee.x - mref;
         const float2 dn2 = make_float2(f, f), nm2 = make_float2(mx, mx);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        constexpr int NCH = C::ST / 16;
+        constexpr int NCH = NT / 16;
         auto expo = [&](int c) {
 #pragma unroll
           for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = __ffma2_rn(x2[k], dn2, nm2);
 #pragma unroll
           for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = make_float2(ex2_ftz(x2[k].x), ex2_ftz(x2[k].y));
         };
-        uint32_t ph[16], pl[C::PP == 2 ? 16 : 1];
+        uint32_t ph[16], pl[16];
         float4 fs[4];
         expo(0);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
           if constexpr (C::COLS) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fs[j] = cm4[C::ST / 4 + 4 * c + j];
+            for (int j = 0; j < 4; ++j) fs[j] = cm4[C::ST / 4 + q0 + 4 * c + j];
           }
           if (c + 1 < NCH) expo(c + 1);
 #pragma unroll
@@ -1286,14 +1297,19 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               }
             }
           }
-          if (c & 1) {
+          if ((c & 1) || NCH == 1) {
             // the last product has read P
-            if (c == 1 && cnt > 0 && !pv_seen) {
+            if (c <= 1 && cnt > 0 && !pv_seen) {
               wait_all(pvdone + x, (cnt - 1) & 1);
               tc_fence_after();
             }
-            tmem_st16(t_p + 8 * (c - 1), ph);
-            if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
+            if constexpr (NCH == 1) {
+              tmem_st8(t_p + col0 / 2, ph);
+              if constexpr (C::PP == 2) tmem_st8(t_p + 32 + col0 / 2, pl);
+            } else {
+              tmem_st16(t_p + 8 * (c - 1), ph);
+              if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
+            }
           }
         }
         const float2 ls2 = __fadd2_rn(ls[0], ls[1]);
@@ -1302,6 +1318,31 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(pready + x, lane);
+      };
+      for (int i = two ? 0 : x; i < nsteps; i += two ? 1 : 2) {
+        const int ck = stage;
+        const uint32_t cpar = phase;
+        const int ahead = two ? 1 : 2;                     // to this slot's next step
+        stage += ahead;
+        if (stage >= C::NC) {
+          stage -= C::NC;
+          phase ^= 1u;
+        }
+        // both at once: they are mostly complete
+        if (!__all_sync(0xffffffffu, mbar_test_wait(sfull + x, cnt & 1) & mbar_test_wait(cfull + ck, cpar))) {
+          wait_all(sfull + x, cnt & 1);
+          wait_all(cfull + ck, cpar);
+        }
+        tc_fence_after();
+        if (!active) {
+          warp_arrive(sfree + x, lane);
+          if (cnt > 0) wait_all(pvdone + x, (cnt - 1) & 1);
+          warp_arrive(pready + x, lane);
+          ++cnt;
+          continue;
+        }
+        if (narrow) softmax_step(std::integral_constant<int, 16>{}, i, ck);
+        else softmax_step(std::integral_constant<int, C::ST>{}, i, ck);
         ++cnt;
         any_step = true;
       }
@@ -1322,26 +1363,78 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // ---- the piece's end: O of the last step
       if (any_step) wait_all(pvdone + x, (cnt - 1) & 1);
       tc_fence_after();
-      float ma = 1.f, mb = 0.f;                            // O = ma O_A + mb O_B (one block of rows)
-      if (!two && active) {
-        if (x == 1) xsum[r] = any_step ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
-        named_bar_sync(pair_bar, 64);
-        if (x == 0) {
-          const float2 o = xsum[r];
-          const float m = fmaxf(m_run, o.x);
-          const float mr = m == -INFINITY ? 0.f : m;
-          ma = ex2_ftz(m_run - mr);
-          mb = ex2_ftz(o.x - mr);
-          l = l * ma + o.y * mb;
-          m_run = m;
+      const bool whole = pw.lo == 0 && pw.hi == pw.count;
+      const int64_t place = int64_t(blockIdx.x) * 2 + (pw.lo == 0 ? 1 : 0);
+      auto out_row = [&](int row) -> int64_t {
+        return int64_t(pw.row0 + token_of(pw, row)) * (bt.Hk << gshift) + head_of(pw, row);
+      };
+      auto v_scale = [&](int d) -> float {
+        if constexpr (C::SI) return __bfloat162float(vs[per_tensor ? 0 : pw.h * D + d]);
+        return 1.f;
+      };
+      if (narrow) {
+        // eight softmaxes of the same rows: their references and sums first, then O
+        // 16 channels at a time, each warp adding up two channels for all rows
+        const int strm = x * 4 + quarter;
+        if (lane < kRgNarrow) xsum[strm * kRgNarrow + lane] = any_step ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+        named_bar_sync(1, 256);
+        const int row = lane & (kRgNarrow - 1);
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, xsum[j * kRgNarrow + row].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 o = xsum[j * kRgNarrow + row];
+          sum += o.y * ex2_ftz(o.x - ref);
         }
-      }
-      if (active) {
-        const bool whole = pw.lo == 0 && pw.hi == pw.count;
-        const int slot = pw.lo == 0 ? 1 : 0;
+        const float mine = any_step ? ex2_ftz(m_run - ref) : 0.f;
+        const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(t_o + 16 * c, ov);
+          tmem_ld_wait();
+          if (lane < kRgNarrow) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              xch[(strm * 16 + e) * kRgNarrow + lane] = any_step ? __uint_as_float(ov[e]) * mine : 0.f;
+          }
+          named_bar_sync(1, 256);
+          const int e = 2 * strm + (lane >> 4), d = 16 * c + e;
+          float o = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o += xch[(j * 16 + e) * kRgNarrow + row];
+          o *= v_scale(d) * inv;
+          if (row < pw.rows) {
+            if (whole) {
+              if constexpr (HP) out[out_row(row) * D + d] = o;
+              else out[out_row(row) * D + d] = __float2bfloat16_rn(o);
+            } else {
+              part_o[(place * D + d) * rows_cap + row] = o;
+            }
+          }
+          named_bar_sync(1, 256);
+        }
+        if (!whole && strm == 0 && lane < pw.rows)
+          *reinterpret_cast<float2*>(part_ml + (place * rows_cap + row) * 2) = make_float2(m, sum);
+      } else if (active) {
+        float ma = 1.f, mb = 0.f;                          // O = ma O_A + mb O_B (one block of rows)
+        if (!two) {
+          if (x == 1) xsum[r] = any_step ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+          named_bar_sync(pair_bar, 64);
+          if (x == 0) {
+            const float2 o = xsum[r];
+            const float m = fmaxf(m_run, o.x);
+            const float mr = m == -INFINITY ? 0.f : m;
+            ma = ex2_ftz(m_run - mr);
+            mb = ex2_ftz(o.x - mr);
+            l = l * ma + o.y * mb;
+            m_run = m;
+          }
+        }
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const int64_t orow = int64_t(pw.row0 + (row_ok ? token_of(pw, rr) : 0)) * (bt.Hk << gshift) + head_of(pw, rr);
-        const int64_t place = int64_t(blockIdx.x) * 2 + slot;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t ov[16];
@@ -1364,13 +1457,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           }
           if (row_ok && (two || x == 0)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y = o[e];
-              if constexpr (C::SI) y *= __bfloat162float(vs[per_tensor ? 0 : pw.h * D + 16 * c + e]);
-              o[e] = y * inv;
-            }
+            for (int e = 0; e < 16; ++e) o[e] *= v_scale(16 * c + e) * inv;
             if (whole) {
-              store_row16(out + orow * D + 16 * c, o);
+              store_row16(out + out_row(rr) * D + 16 * c, o);
             } else {
               // channel by channel, the rows side by side
               float* po = part_o + (place * D + 16 * c) * rows_cap + rr;
@@ -1379,12 +1468,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             }
           }
         }
-        if (!whole && (two || x == 0)) {
-          if (row_ok) *reinterpret_cast<float2*>(part_ml + (place * rows_cap + rr) * 2) = make_float2(m_run, l);
-          if (x == 0 && r == 0) rg_record(pieces + 2 * blockIdx.x + slot, pw.hi == pw.count, pw.row0, pw.n, pw.h, pw.k);
-        }
-        tc_fence_before();
+        if (!whole && row_ok && (two || x == 0))
+          *reinterpret_cast<float2*>(part_ml + (place * rows_cap + rr) * 2) = make_float2(m_run, l);
       }
+      if (!whole && x == 0 && r == 0)
+        rg_record(pieces + place, pw.hi == pw.count, pw.row0, pw.n, pw.h, pw.k);
+      tc_fence_before();
       down = down_n;
       pw = nxt;
       more = more_n;
