@@ -17,14 +17,16 @@
 // is multiplied as it is stored. Running maximum, sum and O are FP32.
 // The scales of the tokens, two ways:
 //   BF16 output: K and V are expanded to code * scale 2^-e (e of the step and of
-//     K or V: 2^e the power of two above the largest scale), rounded to 11 bits;
+//     K or V: 2^e the power of two above the largest scale, less the room that the
+//     codes leave in f16), rounded to 11 bits;
 //     f = 2^eK sm_scale, and P takes 2^eV. P is rounded to 11 bits (BF16 cache:
 //     8). The output itself is rounded to 8. The softmax warps see no scale of a
 //     token: its 64 factors a step and thread, from shared memory, cost them as
 //     much as half of the exponentials.
-//   FP32 output (HP): the codes stay as they are, the scores take the token's K
-//     scale in FP32 and so are those of the dequantized cache, P times the
-//     token's V scale is kept to 22 (16) bits as two parts.
+//   FP32 output (HP): the codes of K stay as they are, and the scores take the
+//     token's K scale in FP32 and so are those of the dequantized cache. The V
+//     scale is parted: its power of two goes into the expanded V (exactly), its
+//     mantissa into P, which is kept to 22 (16) bits as two parts.
 // With static INT8 scales the K scale of each channel multiplies the query (HP:
 // kept as two f16 parts) and the V scale the finished channel.
 //
@@ -92,11 +94,15 @@ struct RgCfg {
   static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
   static constexpr int RPB = QP == 2 ? 128 : 256;                // rows per block
   static constexpr int PP = HP ? 2 : 1;                          // weight parts
+  // The largest scale of a step is expanded to up to 2^UP, which its codes (448, 255 less
+  // the zero point, 57344) leave room for below 65504. BF16 output: a token keeps its 11
+  // bits while its scale is above 2^-(14 + UP) of the step's largest
+  static constexpr int UP = FMT == KVQ_FP8_E4M3 ? 7 : ZP ? 8 : 0;
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
   static constexpr int NC = BF ? NRAW : 3;                       // operand stages
   static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
   static constexpr bool COLS = HP && MV > 0;                     // scores scaled token by token
-  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K, V scale per token; eV, 2^-eV, 2^eK of the step
+  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K scale, V mantissa per token; eV, 2^-eV, 2^eK of the step
   static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
@@ -588,8 +594,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         }
         issued = u + 1;
       }
-      if (lane == 0 && *abort_flag) {
-        // the copies already issued land before the CTA's shared memory goes away
+      if (lane == 0) {
+        // The copies already issued land before the CTA's shared memory goes away. Not
+        // only where a wait has run out by now: another role's may run out later, with
+        // the last copies still on their way.
         volatile int no_abort = 0;
         for (int u = issued > C::NRAW ? issued - C::NRAW : 0; u < issued; ++u)
           mbar_wait(rfull + u % C::NRAW, (u / C::NRAW) & 1, &no_abort, kMmaWaitLimitCycles);
@@ -794,10 +802,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;   // tokens of the page that count
             // f16 pairs of neighbouring tokens' V factors and zero points; K factor and
             // zero point of token `lane % 16`, twice
-            uint32_t vf[C::MV > 0 && !HP ? 8 : 1], vz[C::ZP ? 8 : 1];
+            uint32_t vf[C::MV > 0 ? 8 : 1], vz[C::ZP ? 8 : 1];
             uint32_t kf = 0u, kz = 0u;
             if constexpr (C::MV > 0) {
-              // 2^e above the step's largest finite scale
+              // 2^(e + UP) above the step's largest finite scale
               constexpr int MB = 2 * C::MV;
               auto top_of = [&](const uint8_t* m) -> int {
                 uint32_t top = 0u;
@@ -809,7 +817,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);   // scales are not negative
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
-                return top == 0u ? 0 : min(126, int(top >> 7) - 126);
+                // no scale at all (or tiny ones): 2^-100, which leaves the reference to the
+                // steps whose V counts and keeps the sums of 2^(s - m) finite
+                return top == 0u ? -100 : max(-100, min(126, int(top >> 7) - 126 - C::UP));
               };
               const int ev = top_of(mv), ek = HP ? 0 : top_of(mk);
               const float vdn = __int_as_float((127 - ev) << 23), kdn = __int_as_float((127 - ek) << 23);
@@ -833,7 +843,14 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 #pragma unroll
                 for (int j = 0; j < 8; ++j) out[j] = __shfl_sync(0xffffffffu, two, 2 * j);
               };
-              if constexpr (!HP) {
+              if constexpr (HP) {
+                const int e = max(1, min(253, int(__float_as_uint(sv) >> 23)));   // sv >= 0 or NaN
+                pairs(wild ? sv : __int_as_float(e << 23) * vdn, vf);
+                if (lane < 16) {
+                  cm[t] = sk * qk_scale;
+                  cm[C::ST + t] = wild ? 1.f : sv * __int_as_float((254 - e) << 23);
+                }
+              } else {
                 pairs(sv * vdn, vf);
                 kf = half_bits(sk < INFINITY ? sk * kdn : __int_as_float(0x7fc00000)) * 0x10001u;
               }
@@ -845,12 +862,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                 }
                 pairs(1152.f + zv, vz);
                 kz = half_bits(1152.f + zk) * 0x10001u;
-              }
-              if constexpr (C::COLS) {
-                if (lane < 16) {
-                  cm[t] = sk * qk_scale;
-                  cm[C::ST + t] = sv;
-                }
               }
               if (lane == 0) {
                 if (pw == 0)
@@ -889,7 +900,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               if constexpr (C::ZP) codes16_less_pairs(codes, vz, o0, o1);
               else codes16_to_f16<FMT>(codes, o0, o1);
               uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-              if constexpr (C::MV > 0 && !HP) {
+              if constexpr (C::MV > 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) wv[j] = mul_f16x2(wv[j], vf[j]);
               }
@@ -1018,7 +1029,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           // power-of-two scaling: the largest element lands in [2^14, 2^15)
           int e2 = 0;
           if (amax > 0.f && amax < INFINITY) e2 = 14 - ilogbf(amax);
-          e2 = max(-100, min(100, e2));
+          e2 = max(-113, min(100, e2));
           float up = __int_as_float((127 + e2) << 23);
           if (rg == cs) down = __int_as_float((127 - e2) << 23);
           if constexpr (!C::COLS) {
@@ -1157,7 +1168,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        // HP: the tokens' K and V scales, four at a time; then {eV, 2^-eV, 2^eK}
+        // HP: the tokens' K scales and V mantissas, four at a time; then {eV, 2^-eV, 2^eK}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const int q0 = col0 / 4;
         const uint4 odd = cmask[3 * ck];
@@ -1209,7 +1220,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         }
         float4 ee = make_float4(0.f, 1.f, 1.f, 0.f);       // eV, 2^-eV, 2^eK
         if constexpr (C::MV > 0) ee = cm4[C::COLS ? C::ST / 2 : 0];
-        const float f = C::COLS ? down : down * ee.z;      // takes x to the base-2 score
+        // takes x to the base-2 score; never 0 (a score scale of 0, or an underflow), so that
+        // masked scores stay -inf
+        const float f = fmaxf(C::COLS ? down : down * ee.z, 1.17549435e-38f);
         float mt;
         {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1243,9 +1256,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             tmem_st_wait();
           }
         }
-        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: 2^(x f - m), times
-        // the token's scale)
-        const float mx = HP ? -mref : ee.x - mref;
+        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: times the mantissa of
+        // the token's V scale)
+        const float mx = ee.x - mref;
         const float2 dn2 = make_float2(f, f), nm2 = make_float2(mx, mx);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         constexpr int NCH = NT / 16;
@@ -1310,7 +1323,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           }
         }
         const float2 ls2 = __fadd2_rn(ls[0], ls[1]);
-        l += HP ? ls2.x + ls2.y : (ls2.x + ls2.y) * ee.y;
+        l += (ls2.x + ls2.y) * ee.y;
         if (wild) l = __int_as_float(0x7fc00000);
         tmem_st_wait();
         tc_fence_before();

@@ -30,6 +30,7 @@ Modules
               paged gather + dequantisation.
 ``attention`` FP64 softmax attention over the gathered K/V (GQA head mapping).
 ``sizes``     the closed-form KV-cache byte count.
+``rope``      the rotary embedding of new tokens' query and key rows.
 ``kivi``      KIVI-style low-bit codes (K per channel, V per token, BF16
               residual); the CUDA path for it is not built.
 
@@ -38,4 +39,4 @@ no pin is the quality number (deviation from a BF16-cache attention), which is
 reported, not checked: "parity unpinned".
 """
 
-from . import formats, paged, attention, sizes, kivi  # noqa: F401
+from . import formats, paged, attention, sizes, kivi, rope  # noqa: F401

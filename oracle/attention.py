@@ -98,3 +98,28 @@ def verify_attention(q, kv_per_seq, sm_scale, n_kv_heads):
                 out[b, h, j] = attend_one(q[b, h, j], K[:n, kh, :], V[:n, kh, :], sm_scale)
     return out
 
+
+
+def ragged_attention(q, cu, kv_per_seq, sm_scale, n_kv_heads, window=0):
+    """Outputs [T][Hq][D] float64 of ragged chunks of new tokens.
+
+    q: [T][Hq][D], the new tokens of all sequences one after another; cu [B + 1]:
+    where each sequence's begin. kv_per_seq: list of (K, V), each
+    [ctx_b][n_kv_heads][D]. Row i of sequence b's n rows stands at position
+    p = ctx_b - n + i and attends the tokens t <= p, with a window > 0 those of
+    p - window < t <= p; a row that attends nothing is all zeros. Rows outside
+    [cu[0], cu[B]) are NaN (nobody's)."""
+    q = np.asarray(q, dtype=np.float64)
+    T, Hq, D = q.shape
+    G = Hq // n_kv_heads
+    out = np.full((T, Hq, D), np.nan)
+    for b, (K, V) in enumerate(kv_per_seq):
+        n, ctx = cu[b + 1] - cu[b], K.shape[0]
+        for i in range(n):
+            p = ctx - n + i
+            lo = max(0, p - window + 1) if window else 0
+            for h in range(Hq):
+                kh = h // G
+                out[cu[b] + i, h] = attend_one(q[cu[b] + i, h], K[lo:max(0, p + 1), kh], V[lo:max(0, p + 1), kh],
+                                               sm_scale)
+    return out
