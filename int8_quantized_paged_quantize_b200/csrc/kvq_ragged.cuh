@@ -53,8 +53,8 @@
 //   0       producer: 1-D bulk copies of 4 K and 4 V pages a step into a ring
 //           of raw stages, the scales beside them by plain loads
 //   1       tensor memory, and one thread that issues the products
-//   2       walks the CTA's share of the work list and hands the pieces to the
-//           other roles through a ring; 3: none
+//   2       walks the CTA's share of the work list, hands the pieces to the other
+//           roles through a ring and writes the rows that attend nothing; 3: none
 //   4..7    softmax of slot A (thread = row = TMEM lane), 8..11 of slot B
 //   12..15  converters: codes of a step to f16 (BF16 cache: none), V of tokens
 //           past the end zeroed, the scales as FP32 column factors
@@ -78,6 +78,7 @@
 namespace kvq {
 
 constexpr int kRgRing = 4;                     // pieces handed ahead
+constexpr int kRgGroup = 4;                    // steps of a group of the producer (4 pages a step, a lane each)
 constexpr int kRgNarrow = 16;                  // rows that every warp of a slot has a copy of
 
 template <int D, int FMT, bool HP>
@@ -527,72 +528,91 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------------------------------------------------- producer
+      // Steps go in groups of kRgGroup: a lane holds the block id of one page of a group, two
+      // groups ahead of the copies. The scales of a step are loaded a step ahead. (Pages
+      // asked into L2 a group ahead cost more than they gave: decode of 64 sequences, FP8,
+      // 298 against 262 us.)
       constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
       const int sp = lane / CPP, sc = lane % CPP;
       RgItem it;
       int np = 0, i0 = 0;
       bool more = true;
-      // the next piece with steps
+      struct Group {
+        int id, h, n;                          // this lane's block id (-2: no page), head, steps (0: no more)
+      };
       auto next_item = [&]() {
-        do more = fetch(np++, it, true); while (more && it.count == 0);
+        more = fetch(np++, it, true);
         i0 = it.lo;
       };
-      // block id of page `lane` of step i0 (-2: no page there), and its head
-      int id1 = -2, h1 = 0;
-      auto load_id = [&]() {
-        id1 = -2;
-        h1 = it.h;
-        if (lane >= C::PPS || !more) return;
+      auto next_group = [&]() -> Group {
+        Group g{-2, 0, 0};
+        if (!more) return g;
+        g.h = it.h;
+        g.n = min(kRgGroup, it.hi - i0);
         const int pg = (it.first + i0) * C::PPS + lane;
-        if (int64_t(pg) * kBlockSize < it.ctx) id1 = tables[int64_t(it.b) * bt.W + pg];
+        if (lane < g.n * C::PPS && int64_t(pg) * kBlockSize < it.ctx) g.id = tables[int64_t(it.b) * bt.W + pg];
+        i0 += g.n;
+        if (i0 >= it.hi) next_item();
+        return g;
+      };
+      uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
+      // this lane's chunk of the scales of step j of a group
+      auto scales = [&](const Group& g, int j, uint4& a, uint4& b) {
+        if constexpr (C::MV > 0) {
+          const int blk = __shfl_sync(0xffffffffu, g.id, j * C::PPS + (sp & 3));
+          if (sp < C::PPS && blk >= 0 && blk < NB) {
+            const int64_t off = (int64_t(blk) * bt.Hk + g.h) * C::METAB + sc * 16;
+            a = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ks) + off));
+            b = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(vs) + off));
+          }
+        }
       };
       next_item();
-      load_id();
-      int issued = 0;
-      for (int u = 0, s = 0; more; ++u, s = s + 1 == C::NRAW ? 0 : s + 1) {
-        const uint32_t ph = (u / C::NRAW) & 1;
-        const int id0 = id1, h0 = h1;
-        // the next step's block ids, in flight
-        if (++i0 >= it.hi) next_item();
-        load_id();
-        const bool valid = id0 >= 0 && id0 < NB;
-        if (id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
-        const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
-        const int64_t page = int64_t(id0) * bt.Hk + h0;
-        uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
-        const bool smine = C::MV > 0 && sp < C::PPS && ((mask >> (sp & 3)) & 1u) != 0u;
-        if constexpr (C::MV > 0) {
-          const int sblk = __shfl_sync(0xffffffffu, id0, sp & 3);
-          if (smine) {
-            const int64_t off = (int64_t(sblk) * bt.Hk + h0) * C::METAB + sc * 16;
-            kv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ks) + off));
-            vv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(vs) + off));
+      Group cur = next_group(), nxt = next_group();
+      scales(cur, 0, kv, vv);
+      int issued = 0, s = 0;
+      bool ok = true;
+      while (ok && cur.n > 0) {
+        const Group far = next_group();
+        for (int j = 0; j < cur.n; ++j, s = s + 1 == C::NRAW ? 0 : s + 1) {
+          const int u = issued;
+          const int id0 = __shfl_sync(0xffffffffu, cur.id, j * C::PPS + (lane & 3));
+          const bool valid = lane < C::PPS && id0 >= 0 && id0 < NB;
+          if (lane < C::PPS && id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
+          const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
+          const int64_t page = int64_t(id0) * bt.Hk + cur.h;
+          uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;
+          if (j + 1 < cur.n) scales(cur, j + 1, kn, vn);
+          else scales(nxt, 0, kn, vn);
+          if (lane == 0) {
+            ok = u < C::NRAW || mbar_wait(rfree + s, ((u / C::NRAW) & 1) ^ 1, abort_flag, wait_limit);
+            if (ok) mbar_expect_tx(rfull + s, 2u * uint32_t(__popc(mask)) * uint32_t(C::PAGE));
           }
-        }
-        bool ok = true;
-        if (lane == 0) {
-          ok = u < C::NRAW || mbar_wait(rfree + s, ph ^ 1, abort_flag, wait_limit);
-          if (ok) mbar_expect_tx(rfull + s, 2u * uint32_t(__popc(mask)) * uint32_t(C::PAGE));
-        }
-        if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
-        uint8_t* st = raw + s * C::RSTAGE;
-        if (valid) {
-          bulk_g2s_keep(st + lane * C::PAGE, kc + page * C::PAGE, C::PAGE, rfull + s);
-          bulk_g2s_keep(st + (C::PPS + lane) * C::PAGE, vc + page * C::PAGE, C::PAGE, rfull + s);
-        }
-        if constexpr (C::MV > 0) {
-          if (smine) {
-            uint8_t* m = rmeta + s * C::RMETA;
-            *reinterpret_cast<uint4*>(m + sp * C::METAB + sc * 16) = kv;
-            *reinterpret_cast<uint4*>(m + (C::PPS + sp) * C::METAB + sc * 16) = vv;
+          ok = __shfl_sync(0xffffffffu, int(ok), 0);
+          if (!ok) break;
+          uint8_t* st = raw + s * C::RSTAGE;
+          if (valid) {
+            bulk_g2s_keep(st + lane * C::PAGE, kc + page * C::PAGE, C::PAGE, rfull + s);
+            bulk_g2s_keep(st + (C::PPS + lane) * C::PAGE, vc + page * C::PAGE, C::PAGE, rfull + s);
           }
+          if constexpr (C::MV > 0) {
+            if (sp < C::PPS && ((mask >> (sp & 3)) & 1u) != 0u) {
+              uint8_t* m = rmeta + s * C::RMETA;
+              *reinterpret_cast<uint4*>(m + sp * C::METAB + sc * 16) = kv;
+              *reinterpret_cast<uint4*>(m + (C::PPS + sp) * C::METAB + sc * 16) = vv;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            rmask[s] = mask;
+            mbar_arrive(rfull + s);
+          }
+          issued = u + 1;
+          kv = kn;
+          vv = vn;
         }
-        __syncwarp();
-        if (lane == 0) {
-          rmask[s] = mask;
-          mbar_arrive(rfull + s);
-        }
-        issued = u + 1;
+        cur = nxt;
+        nxt = far;
       }
       if (lane == 0) {
         // The copies already issued land before the CTA's shared memory goes away. Not
@@ -667,7 +687,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       RgItem w;
       for (int np = 0; ok && fetch(np, w, false); ++np) {
         const int steps = w.hi - w.lo;
-        if (steps == 0) continue;
         const bool two = w.rows > 128;
         ok = wait(qready, par_q);
         par_q ^= 1u;
@@ -697,21 +716,40 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       mbar_wait(drain, 0, &no_abort, kMmaWaitLimitCycles);
       }
       __syncwarp();
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2) {
       // ---------------------------------------------------------- the pieces
+      // The whole warp walks, all lanes alike. Blocks in which no row attends anything get
+      // their zero rows here and are not handed on: a role looks at most kRgRing pieces
+      // ahead of the one that it holds up, so it may not skip any number of them.
+      using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
       RgWalk w;
       w.init(bt, misci[0], miscll[0], start, end);
-      for (int i = 0;; ++i) {
+      for (int i = 0;; w.next(bt)) {
+        if (!w.done && w.count == 0) {
+          constexpr int PER = D * int(sizeof(OutT)) / 16;      // 16-byte pieces of a row
+          for (int j = lane; j < w.rows * PER; j += 32) {
+            const int rr = j / PER;
+            const int64_t row = int64_t(w.row0 + (w.k << bt.p.pos_log) + (rr >> bt.p.g_log)) * (bt.Hk << bt.p.g_log) +
+                                (w.h << bt.p.g_log) + (rr & ((1 << bt.p.g_log) - 1));
+            reinterpret_cast<uint4*>(static_cast<OutT*>(out_) + row * D)[j % PER] = make_uint4(0, 0, 0, 0);
+          }
+          continue;
+        }
         const int s = i % kRgRing;
-        if (i >= kRgRing && !mbar_wait(pfree + s, (i / kRgRing - 1) & 1, abort_flag, wait_limit)) break;
-        RgItem it;
-        it.b = w.b; it.h = w.h; it.k = w.k; it.rows = w.done ? 0 : w.rows;
-        it.row0 = w.row0; it.n = w.s.n; it.ctx = w.s.ctx; it.first = w.first;
-        it.lo = w.lo; it.hi = w.hi; it.count = w.count; it.pad = 0;
-        items[s] = it;
-        mbar_arrive(pfull + s);
-        if (w.done) break;
-        w.next(bt);
+        bool got = true;
+        if (lane == 0) {
+          got = i < kRgRing || mbar_wait(pfree + s, (i / kRgRing - 1) & 1, abort_flag, wait_limit);
+          if (got) {
+            RgItem it;
+            it.b = w.b; it.h = w.h; it.k = w.k; it.rows = w.done ? 0 : w.rows;
+            it.row0 = w.row0; it.n = w.s.n; it.ctx = w.s.ctx; it.first = w.first;
+            it.lo = w.lo; it.hi = w.hi; it.count = w.count; it.pad = 0;
+            items[s] = it;
+            mbar_arrive(pfull + s);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, int(got), 0) || w.done) break;
+        ++i;
       }
     }
   } else if (warp >= 12) {
@@ -1092,29 +1130,19 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         st32(dst, v);
       }
     };
-    // The next piece with steps; blocks in which no row attends anything get
-    // their zero rows here. The eight warps meet at barriers, so they go on
-    // together or not at all.
+    // The next piece. The eight warps meet at barriers, so they go on together or
+    // not at all.
     int np = 0;
     auto next_item = [&](RgItem& w) -> bool {
-      while (true) {
-        const bool mine = ok && fetch(np++, w, true);
-        uint32_t both;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-            : "=r"(both)
-            : "r"(uint32_t(mine))
-            : "memory");
-        if (both == 0u) return false;
-        if (w.count > 0) return true;
-        const int rr = block_row(w);
-        if (rr < w.rows && (w.rows > 128 || (x == 0 && (w.rows > kRgNarrow || quarter == 0)))) {
-          OutT* dst = out + (int64_t(w.row0 + token_of(w, rr)) * (bt.Hk << gshift) + head_of(w, rr)) * D;
-          const float z[16] = {};
-          for (int c = 0; c < D / 16; ++c) store_row16(dst + 16 * c, z);
-        }
-      }
+      const bool mine = ok && fetch(np++, w, true);
+      uint32_t both;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+          : "=r"(both)
+          : "r"(uint32_t(mine))
+          : "memory");
+      return both != 0u;
     };
 
     RgItem pw;

@@ -84,6 +84,19 @@ def test_more_new_tokens_than_context(fmt):
             assert dead == n[b] or torch.count_nonzero(out[cu[b] + dead]) > 0
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+def test_runs_of_rows_that_attend_nothing(fmt):
+    """Many blocks in a row without a token to attend, between others, in the share of one
+    CTA: no role may wait for a piece that another reaches only later."""
+    ctx = [200] + [0] * 30 + [64, 1] + [0] * 9 + [130] + [0] * 40
+    n = [3] + [1] * 30 + [64, 2] + [5] * 9 + [1] + [2] * 40
+    f = SC.Filled(fmt, ctx, Hk=8, G=1, D=64)
+    run(f, n)
+    run(f, n[::-1], check=False)
+    f = SC.Filled(fmt, [0] * 20 + [50] * 300 + [0] * 20, Hk=4, G=2, D=64)   # one step a piece
+    run(f, [1] * 340)
+
+
 @pytest.mark.parametrize("fmt,f32", [("fp8", False), ("int8", True), ("int8t", False)])
 def test_one_long_sequence(fmt, f32):
     """A context that is cut into pieces over many CTAs and joined, alone on the grid:
