@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -54,6 +55,23 @@ static inline cudaError_t read_error_word(uint32_t* flags, int clear) {
   }
   return e;
 }
+
+// What is set up once per context (a new one, after a device reset, has another
+// id): the attributes of a kernel, which cost as much as a launch to set.
+class OncePerContext {
+ public:
+  bool done(int dev) const {
+    const unsigned long long id = context_id();
+    return id != 0 && dev < 64 && ids_[dev].load(std::memory_order_acquire) == id;
+  }
+  void set(int dev) {
+    const unsigned long long id = context_id();
+    if (id != 0 && dev < 64) ids_[dev].store(id, std::memory_order_release);
+  }
+
+ private:
+  std::atomic<unsigned long long> ids_[64] = {};
+};
 
 // Launch as the programmatic dependent of the kernel ahead on the stream: it
 // may start (and run up to its grid_dep_wait) before that kernel finishes.

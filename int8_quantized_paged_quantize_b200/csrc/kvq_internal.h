@@ -97,7 +97,7 @@ int launch_prefill_partial(const void* q, int32_t B, const void* kc, const void*
                            void* stream, int n_query);
 int launch_decode_merge(int32_t B, const int32_t* ctx, int32_t max_ctx, void* out, bool out_f32,
                         const void* ws, const DecodePlan& plan, const kvq_dims& d, void* stream,
-                        int rows_per_count = 0);
+                        int rows_per_count = 0, const int32_t* dst_row = nullptr);
 // The write with rotary embedding: strided rows, positions and angles.
 struct RopeArgs {
   const void *q, *k, *v;

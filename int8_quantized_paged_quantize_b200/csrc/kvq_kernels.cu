@@ -68,16 +68,22 @@ cudaError_t decode_mma_dispatch3(const void* q, int32_t B, const void* kc, const
                                  int per_tensor, int n_query, int nrg, cudaStream_t st) {
   using C = MmaCfg<D, G, FMT>;
   auto kern = decode_mma_kernel<D, G, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static OncePerContext once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           int(cudaSharedmemCarveoutMaxShared));
-  if (e != cudaSuccess) return e;
+  if (!once.done(dev)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             int(cudaSharedmemCarveoutMaxShared));
+    if (e != cudaSuccess) return e;
+    once.set(dev);
+  }
   // resident CTAs per SM: shared memory bounds it (registers are capped so
   // that two 8-bit CTAs fit); the BF16 ring takes a whole SM
-  int dev = 0, smem_sm = 0, reserved = 0;
-  e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  int smem_sm = 0, reserved = 0;
+  e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
   if (e != cudaSuccess) return e;
   const int per_sm = std::max(1, std::min(FMT == KVQ_BF16 ? 1 : 2, smem_sm / (C::SMEM + reserved)));
@@ -222,7 +228,7 @@ int launch_decode_partial(const void* q, int32_t B, const void* kc, const void* 
 
 int launch_decode_merge(int32_t B, const int32_t* ctx, int32_t max_ctx, void* out, bool out_f32,
                         const void* ws, const DecodePlan& plan, const kvq_dims& d, void* stream,
-                        int rows_per_count) {
+                        int rows_per_count, const int32_t* dst_row) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const float* po = static_cast<const float*>(ws);
   const float* pml = reinterpret_cast<const float*>(static_cast<const char*>(ws) + plan.o_bytes);
@@ -238,17 +244,17 @@ int launch_decode_merge(int32_t B, const int32_t* ctx, int32_t max_ctx, void* ou
   if (d.head_dim == 128) {
     if (out_f32)
       e = launch_pdl(merge_kernel<128, float>, grid, dim3(128), 0, st, ctx, Hq, G, plan.slots,
-                     max_ctx, W, po, pml, pcnt, static_cast<float*>(out), rows);
+                     max_ctx, W, po, pml, pcnt, static_cast<float*>(out), rows, dst_row);
     else
       e = launch_pdl(merge_kernel<128, __nv_bfloat16>, grid, dim3(128), 0, st, ctx, Hq, G,
-                     plan.slots, max_ctx, W, po, pml, pcnt, static_cast<__nv_bfloat16*>(out), rows);
+                     plan.slots, max_ctx, W, po, pml, pcnt, static_cast<__nv_bfloat16*>(out), rows, dst_row);
   } else {
     if (out_f32)
       e = launch_pdl(merge_kernel<64, float>, grid, dim3(128), 0, st, ctx, Hq, G, plan.slots,
-                     max_ctx, W, po, pml, pcnt, static_cast<float*>(out), rows);
+                     max_ctx, W, po, pml, pcnt, static_cast<float*>(out), rows, dst_row);
     else
       e = launch_pdl(merge_kernel<64, __nv_bfloat16>, grid, dim3(128), 0, st, ctx, Hq, G,
-                     plan.slots, max_ctx, W, po, pml, pcnt, static_cast<__nv_bfloat16*>(out), rows);
+                     plan.slots, max_ctx, W, po, pml, pcnt, static_cast<__nv_bfloat16*>(out), rows, dst_row);
   }
   if (e != cudaSuccess) return int(e);
   return int(cudaGetLastError());

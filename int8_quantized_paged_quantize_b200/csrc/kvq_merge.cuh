@@ -11,7 +11,8 @@ namespace kvq {
 // partials (m_i, l_i, o_i) as m = max m_i, l = sum l_i 2^(m_i - m),
 // o = sum o_i 2^(m_i - m) / l. Lane i holds slot i's (m, l) (32 slots at a
 // time); each lane owns D/32 consecutive channels and reads them as one vector
-// per slot, so a row's partials stream in with every load in flight.
+// per slot, so a row's partials stream in with every load in flight. dst_row:
+// the output token of each sequence (negative: not written), null: its index.
 template <int D>
 struct MergeVec {
   static constexpr int N = D / 32;
@@ -33,7 +34,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const int32_t* __restrict__ 
                                                     const float* __restrict__ part_o,
                                                     const float* __restrict__ part_ml,
                                                     const int32_t* __restrict__ part_cnt,
-                                                    OutT* __restrict__ out, int rows) {
+                                                    OutT* __restrict__ out, int rows,
+                                                    const int32_t* __restrict__ dst_row) {
   constexpr int N = D / 32;
   constexpr int PRE = 8;                                   // slots whose vectors load up front
   const int lane = threadIdx.x & 31;
@@ -110,7 +112,13 @@ __global__ void __launch_bounds__(128) merge_kernel(const int32_t* __restrict__ 
   float r[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = l != 0.f ? o[i] / l : 0.f;
-  OutT* dst = out + int64_t(bq) * D + lane * N;
+  int64_t row = bq;
+  if (dst_row) {                                           // sequence b's rows go elsewhere, or nowhere
+    const int to = dst_row[b];
+    if (to < 0) return;
+    row = int64_t(to) * Hq + bq % Hq;
+  }
+  OutT* dst = out + row * D + lane * N;
   if constexpr (sizeof(OutT) == 4) {
     if constexpr (N == 4) *reinterpret_cast<float4*>(dst) = make_float4(r[0], r[1], r[2], r[3]);
     else *reinterpret_cast<float2*>(dst) = make_float2(r[0], r[1]);

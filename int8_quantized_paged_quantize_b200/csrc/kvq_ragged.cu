@@ -24,10 +24,37 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Workspace pieces: two places per CTA of `rows` rows each.
+// A call with one new token a sequence and no window is a decode step: its single
+// tokens go through the decode kernels, which multiply the codes as they are stored (64
+// sequences of 1,024 to 8,192 tokens, 32/8 heads, FP8: 100 us against 270 us of the
+// ragged kernel, whose converters and producer take 1,800 cycles a step however few
+// rows there are; 3 of up to 8,192, 8 KV heads: 22 against 38 us; 1 of 100, 1 KV head: 14
+// against 14 us). Not with FP8 and FP32 output, where their weights would have 18 bits
+// instead of 22; nor with contexts above kRtLong for each (sequence, KV head), of which
+// the decode kernels' at most 15 splits leave SMs idle (1 of 60,000 tokens, 1 KV head: 56
+// against 47 us).
+constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
+constexpr int64_t kRtLong = 32768;
+
+// The decode kernels' plan: at most kRtSlots partials a row (the automatic plan's
+// number), and kRtRows of them over all sequences.
+int rt_plan(int32_t n, int32_t max_ctx, const kvq_dims& d, DecodePlan* plan) {
+  const int32_t tiles = std::max(1, (max_ctx + kTileTokens - 1) / kTileTokens);
+  const int32_t splits = std::min(kRtSlots, kRtRows / n) - 1;
+  return make_plan(n, max_ctx, kTileTokens * ((tiles + splits - 1) / splits), &d, plan);
+}
+// Its workspace for up to n sequences (not falling with n).
+size_t rt_bytes(int32_t n, const kvq_dims& d) {
+  const size_t rows = size_t(std::min(n * kRtSlots, kRtRows)) * d.n_q_heads;
+  return round256(rows * d.head_dim * sizeof(float)) + round256(rows * 2 * sizeof(float)) +
+         round256(size_t(n) * d.n_q_heads * sizeof(int32_t));
+}
+
+// Workspace pieces: two places per CTA of `rows` rows each; for a decode step each
+// sequence's context and output row, its query and the decode kernels' workspace.
 struct RgSpace {
   int rows;
-  size_t o, ml, total;
+  size_t o, ml, pieces, seqs, q1, total;
 };
 RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   RgSpace w;
@@ -36,34 +63,37 @@ RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   const size_t places = 2 * size_t(device_sm_count());
   w.o = round256(places * w.rows * d.head_dim * sizeof(float));
   w.ml = round256(places * w.rows * 2 * sizeof(float));
-  w.total = w.o + w.ml + round256(places * sizeof(RgPiece));
+  w.pieces = round256(places * sizeof(RgPiece));
+  w.total = w.o + w.ml + w.pieces;
+  const int32_t n = std::min(total_q, kRtSeqs);
+  w.seqs = round256(size_t(n) * sizeof(int32_t));
+  w.q1 = round256(size_t(n) * d.n_q_heads * d.head_dim * 2);
+  w.total += 2 * w.seqs + w.q1 + rt_bytes(n, d);
   return w;
 }
 
 // Shared-memory limit of the kernel, and the check that its registers are those
-// that it shares out anew. Both cost as much as a launch, so they are done once
-// per context (a new one, after a reset, has another id).
+// that it shares out anew.
 template <int D, int FMT, bool HP>
 cudaError_t prepare() {
   auto kern = ragged_mma_kernel<D, FMT, HP>;
-  static std::atomic<unsigned long long> done[64];
+  static OncePerContext once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned long long id = context_id();
-  if (id != 0 && dev < 64 && done[dev].load(std::memory_order_acquire) == id) return cudaSuccess;
+  if (once.done(dev)) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RgCfg<D, FMT, HP>::SMEM);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kRgRegs) return cudaErrorInvalidConfiguration;
-  if (id != 0 && dev < 64) done[dev].store(id, std::memory_order_release);
+  once.set(dev);
   return cudaSuccess;
 }
 
 template <int D, int FMT, bool HP>
-cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tensor, cudaStream_t st) {
+cudaError_t ragged_dispatch(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d, int per_tensor, cudaStream_t st) {
   using C = RgCfg<D, FMT, HP>;
   using OutT = typename std::conditional<HP, float, __nv_bfloat16>::type;
   auto kern = ragged_mma_kernel<D, FMT, HP>;
@@ -86,6 +116,18 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
   b.p.g_log = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
   b.p.pos_log = (C::RPB == 256 ? 8 : 7) - b.p.g_log;
   b.p.window = a.window;
+  b.ctx1 = b.row1 = nullptr;
+  b.q1 = nullptr;
+  DecodePlan plan;
+  const bool step = !(HP && C::F8) && a.window == 0 && a.total_q == a.n_seqs && a.n_seqs <= kRtSeqs &&
+                    a.max_ctx <= kRtLong * a.n_seqs * d.n_kv_heads && rt_plan(a.n_seqs, a.max_ctx, d, &plan) == KVQ_OK &&
+                    plan.total <= rt_bytes(a.n_seqs, d);
+  char* at = ws + w.o + w.ml + w.pieces;
+  if (step) {
+    b.ctx1 = reinterpret_cast<int32_t*>(at);
+    b.row1 = reinterpret_cast<int32_t*>(at + w.seqs);
+    b.q1 = reinterpret_cast<uint4*>(at + 2 * w.seqs);
+  }
   const int grid = device_sm_count();                    // one CTA per SM
   e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kRgThreads), C::SMEM, st,
                  static_cast<const __nv_bfloat16*>(a.q), a.q_stride, static_cast<const uint8_t*>(a.kc),
@@ -97,7 +139,12 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, const kvq_dims& d, int per_tens
                  dim3(256), 0, st, static_cast<const float*>(po), static_cast<const float*>(pml),
                  static_cast<const RgPiece*>(pieces), grid, w.rows, b.p, int(d.n_q_heads),
                  static_cast<OutT*>(a.out));
-  return e;
+  if (e != cudaSuccess || !step) return e;
+  void* dws = at + 2 * w.seqs + w.q1;
+  e = cudaError_t(launch_decode_partial(b.q1, a.n_seqs, a.kc, a.vc, a.ks, a.vs, a.tables, b.ctx1, a.max_ctx, a.sm_scale, plan, dws,
+                                        fmt, d, st, 1));
+  if (e != cudaSuccess) return e;
+  return cudaError_t(launch_decode_merge(a.n_seqs, b.ctx1, a.max_ctx, a.out, a.out_f32, dws, plan, d, st, 0, b.row1));
 }
 }  // namespace
 
@@ -108,7 +155,7 @@ int launch_ragged(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d, void* str
   const int pt = fmt == KVQ_INT8_TENSOR;
   cudaError_t e;
 #define KVQ_RG(DD, FF) \
-  e = a.out_f32 ? ragged_dispatch<DD, FF, true>(a, d, pt, st) : ragged_dispatch<DD, FF, false>(a, d, pt, st)
+  e = a.out_f32 ? ragged_dispatch<DD, FF, true>(a, fmt, d, pt, st) : ragged_dispatch<DD, FF, false>(a, fmt, d, pt, st)
 #define KVQ_RG_D(DD)                                       \
   switch (fmt) {                                           \
     case KVQ_FP8_E4M3: KVQ_RG(DD, KVQ_FP8_E4M3); break;    \

@@ -144,11 +144,15 @@ struct RgBatch {
   const int32_t* cu;
   const int32_t* ctx_lens;
   int B, T, Hk, W, max_ctx;
+  // null, or (a decode step) the sequences with one new token are the decode kernels':
+  // their context (0 for the others), output row (-1) and query row, for these to read
+  int32_t *ctx1, *row1;
+  uint4* q1;
   RgShape p;
 
   // sequence b: its new tokens and context; a range or a context that is not
   // legal counts as empty
-  __device__ __forceinline__ RgSeq seq(int b, int* row0, unsigned* bad) const {
+  __device__ __forceinline__ RgSeq seq(int b, int* row0, unsigned* bad, bool all = false) const {
     const int c0 = cu[b], c1 = cu[b + 1], x = ctx_lens[b];
     RgSeq s;
     s.n = c1 - c0;
@@ -162,6 +166,7 @@ struct RgBatch {
       f |= KVQ_DEVERR_CONTEXT;
       s.ctx = 0;
     }
+    if (!all && ctx1 && s.n == 1) s.n = 0;
     *row0 = c0;
     if (bad) *bad = f;
     return s;
@@ -455,6 +460,21 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
   // the kernel ahead on the stream has finished
   grid_dep_wait();
   grid_dep_launch_dependents();
+
+  if (bt.ctx1) {
+    const int n16 = (bt.Hk << bt.p.g_log) * D / 8;         // 16-byte pieces of a query row
+    for (int b = blockIdx.x; b < bt.B; b += gridDim.x) {
+      int row0;
+      const RgSeq sq = bt.seq(b, &row0, nullptr, true);
+      const bool one = sq.n == 1;
+      if (threadIdx.x == 0) {
+        bt.ctx1[b] = one ? sq.ctx : 0;
+        bt.row1[b] = one ? row0 : -1;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(q + int64_t(row0) * q_stride);
+      for (int i = threadIdx.x; one && i < n16; i += kRgThreads) bt.q1[int64_t(b) * n16 + i] = src[i];
+    }
+  }
 
   // ------------------------------------------------------------ the share
   // Each thread has one sequence (or, in rounds, every 512th): its cost, the

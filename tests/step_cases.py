@@ -27,11 +27,11 @@ class Filled:
     sequence has, table entries behind a context and tokens behind it in its last
     page hold NaN patterns (codes and scales), which no result may show."""
 
-    def __init__(self, fmt, ctx, Hk=2, G=2, D=64, seed=0, scale=1.0, row_scale=None, extra=3):
+    def __init__(self, fmt, ctx, Hk=2, G=2, D=64, seed=0, scale=1.0, row_scale=None, extra=3, width=0):
         rng = np.random.default_rng([seed, Hk, G, D])
         self.fmt, self.ctx, self.Hk, self.G, self.D = fmt, list(ctx), Hk, G, D
         pages = [(c + 15) // 16 for c in ctx]
-        nb, W = sum(pages) + extra, max(pages + [1]) + 1
+        nb, W = sum(pages) + extra, max(pages + [1, width - 1]) + 1
         perm = rng.permutation(nb)
         self.tables = np.full((len(ctx), W), perm[-1], dtype=np.int32)      # a block of nobody
         at = 0
@@ -79,7 +79,7 @@ class Filled:
         return max(self.ctx + [1])
 
 
-def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32):
+def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32, step=False):
     """(out, bound) [T][Hq][D] float64 of ragged attention: the value, and how far the
     kernel may be from it by its stated roundings:
       scores   FP32 output: the operands are exact (static INT8: the query times the
@@ -100,7 +100,13 @@ def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32):
       2^-25 sum_t |V_t| 2^-e(t) * 2^m / sum_u 2^s(u),   m <= max_u (s(u) + e(u)),
     and with 2^m <= sum_u 2^(s(u) + e(u)):  2^-25 sum_t |V_t| 2^-e(t) * sum_u w_u 2^e(u).
     2^e is a power of two above the step's largest scale, less a constant: at most twice
-    as far apart between two steps as the scales are, hence the factor 2."""
+    as far apart between two steps as the scales are, hence the factor 2.
+
+    step: a decode step with an INT8 cache, whose decode kernel holds a weight times its
+    token's scale as 24 bits of fixed point below the largest weight times the largest
+    scale of a tile of 128 tokens: in the output
+      2^-24 w_max sum_t (s_max / s_t) |V_t|,
+    and scales are at most twice as far apart as the rows' largest values."""
     q = np.asarray(q, dtype=np.float64)
     T, Hq, D = q.shape
     G = Hq // Hk
@@ -133,6 +139,10 @@ def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32):
                 out[r, h] = w @ vv
                 a = w @ np.abs(vv)
                 bound[r, h] = a * (np.expm1(2 * d) + dp + dv + 2.0 ** -20) * 1.01 + np.abs(out[r, h]) * do + 1e-30
+                if step and fmt == "int8":
+                    size = np.maximum(np.abs(v[:p + 1]).max(-1), 1e-30)
+                    far = np.concatenate([size[t:t + 128].max() / size[t:t + 128] for t in range(0, p + 1, 128)])
+                    bound[r, h] += 2.0 ** -23 * w.max() * (far @ np.abs(v[:p + 1]))
                 if fmt != "bf16":
                     bound[r, h] += 2.0 ** -24 * ((1 / top[lo:p + 1]) @ np.abs(vv)) * (w @ top[lo:p + 1])
     return out, bound

@@ -29,7 +29,8 @@ def run(f, n, window=0, f32=True, sm=None, q=None, check=True, seed=1, note="", 
                          out_dtype=torch.float32 if f32 else torch.bfloat16, **kw)
     assert kvq.device_error() == 0
     if check:
-        SC.assert_within(out, *SC.attention_and_bound(q, cu, f.kv(), sm, f.Hk, window, f.fmt, f32), note=note)
+        step = int(cu[-1]) == len(n) and window == 0
+        SC.assert_within(out, *SC.attention_and_bound(q, cu, f.kv(), sm, f.Hk, window, f.fmt, f32, step), note=note)
     return out
 
 
@@ -228,6 +229,109 @@ def test_agrees_with_decode_and_prefill():
     qp = SC.bf16(q).cuda().view(4, 30, 8, 128).transpose(1, 2).contiguous()
     b = f.cache.prefill(qp, f.d_tables, SC.i32(f.ctx), f.max_ctx, out_dtype=torch.float32)
     assert (a - b).abs().max() < 2e-5
+
+
+# ------------------------------------------------------------------ decode steps
+# As many new tokens as sequences and no window: the call's single tokens go through the
+# decode kernels (8-bit floats: with BF16 output).
+STEP_LEN = 16 * 80
+
+
+def decode_step(fmt, G=2, D=64, seed=0, B=64, Hk=8):
+    rng = np.random.default_rng([seed, G])
+    ctx = [int(x) for x in rng.choice([0, 1, 16, 17, 100, 128, 129, 300], B)]
+    ctx[5], ctx[-1] = 900, 131
+    return SC.Filled(fmt, ctx, Hk=Hk, G=G, D=D, width=STEP_LEN // 16, seed=seed)
+
+
+def step_call(f, n, q, tables=None, ctx=None, **kw):
+    cu = np.concatenate([[0], np.cumsum(n)])
+    return f.cache.ragged(q if isinstance(q, torch.Tensor) else SC.bf16(q).cuda(), SC.i32(cu), f.d_tables if tables is None else tables,
+                          SC.i32(f.ctx if ctx is None else ctx), STEP_LEN, **kw)
+
+
+@pytest.mark.parametrize("fmt", SC.ALL)
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 2), (64, 4), (128, 8)])
+def test_decode_steps(fmt, D, G):
+    """One token a sequence; and the same shape of call with sequences that bring none or
+    several beside it."""
+    f = decode_step(fmt, G=G, D=D, B=64 if G < 8 else 24, Hk=8 if G < 8 else 17)
+    B = len(f.ctx)
+    rng = np.random.default_rng(G)
+    q = query(rng, B, f)
+    mixed = [1] * B
+    mixed[0], mixed[1], mixed[2], mixed[7], mixed[8], mixed[B - 1] = 0, 2, 0, 0, 3, 0
+    for n in ([1] * B, mixed):
+        m = sum(n)
+        for f32 in (False, True):
+            out = step_call(f, n, q, out_dtype=torch.float32 if f32 else torch.bfloat16)
+            assert kvq.device_error() == 0
+            ref, bound = SC.attention_and_bound(q[:m], np.concatenate([[0], np.cumsum(n)]), f.kv(), D ** -0.5, f.Hk, 0, fmt, f32)
+            SC.assert_within(out[:m], ref, bound)
+
+
+def test_decode_steps_that_are_not_legal_or_not_whole():
+    """Contexts, ranges and block ids that are not legal, rows of nobody, a strided query."""
+    f = decode_step("fp8")
+    B, rng = len(f.ctx), np.random.default_rng(1)
+    fused = SC.bf16(rng.standard_normal((B, 16 + 16, 64)).astype(np.float32)).cuda()
+    q = fused[:, :16]
+    base = step_call(f, [1] * B, q)
+    assert kvq.device_error() == 0
+    ctx = list(f.ctx)
+    ctx[3], ctx[4] = -1, STEP_LEN + 1
+    out = step_call(f, [1] * B, q, ctx=ctx)
+    assert kvq.device_error() == kvq.DEVERR_CONTEXT
+    assert torch.count_nonzero(out[3:5]) == 0 and torch.equal(out[:3], base[:3]) and torch.equal(out[5:], base[5:])
+    out = torch.full_like(base, 7.0)                 # the last ten sequences have no tokens
+    cu = np.minimum(np.arange(B + 1), B - 10)
+    f.cache.ragged(q, SC.i32(cu), f.d_tables, SC.i32(f.ctx), STEP_LEN, out=out)
+    assert kvq.device_error() == 0 and torch.equal(out[:B - 10], base[:B - 10]) and (out[B - 10:] == 7).all()
+    cu = np.arange(B + 1)
+    cu[9] = 100                                      # falls again: two ranges that are not
+    out.fill_(7.0)
+    f.cache.ragged(q, SC.i32(cu), f.d_tables, SC.i32(f.ctx), STEP_LEN, out=out)
+    assert kvq.device_error() == kvq.DEVERR_RANGE
+    assert (out[8:10] == 7).all() and torch.equal(out[:8], base[:8]) and torch.equal(out[10:], base[10:])
+    t = f.tables.copy()
+    t[5, :57] = -1                                   # all pages of sequence 5, one of the last
+    t[B - 1, 8] = f.nb
+    out = step_call(f, [1] * B, q, tables=torch.from_numpy(t).cuda())
+    assert kvq.device_error() == kvq.DEVERR_BLOCK
+    assert torch.count_nonzero(out[5]) == 0 and torch.equal(out[:5], base[:5]) and torch.equal(out[6:B - 1], base[6:B - 1])
+    K, V = f.kv()[B - 1]
+    ref, bound = SC.attention_and_bound(q[B - 1:].float().cpu().numpy(), [0, 1], [(K[:128], V[:128])], 0.125, 8, 0, "fp8", False)
+    SC.assert_within(out[B - 1:], ref, bound)
+
+
+def test_a_captured_decode_step():
+    """A graph of a decode step, replayed as one and as a step of another make-up."""
+    f = decode_step("int8", G=4)
+    B, rng = len(f.ctx), np.random.default_rng(2)
+    ws = f.cache.ragged_workspace(B)
+    q, out = SC.bf16(query(rng, B, f)).cuda(), torch.zeros(B, 32, 64, dtype=torch.bfloat16, device="cuda")
+    cu, ctx = SC.i32(np.arange(B + 1)), SC.i32(f.ctx)
+    call = lambda: f.cache.ragged(q, cu, f.d_tables, ctx, STEP_LEN, out=out, workspace=ws)  # noqa: E731
+    call()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    n = [0] * B
+    n[5], n[-1] = 60, 4
+    c0 = np.concatenate([[0], np.cumsum(n)])
+    cu.copy_(SC.i32(c0))
+    g.replay()
+    assert kvq.device_error() == 0
+    ref, bound = SC.attention_and_bound(q.float().cpu().numpy(), c0, f.kv(), 0.125, 8, 0, "int8", False)
+    SC.assert_within(out, ref, bound)
+    cu.copy_(SC.i32(np.arange(B + 1)))
+    g.replay()
+    assert torch.equal(out, want)
 
 
 # ------------------------------------------------------------------ bad input on the device

@@ -109,8 +109,8 @@ def test_ragged_of_nothing_and_its_workspace():
         assert ragged(win=-1, **none) == ARG
     size = lambda n, fmt=1, d=DIMS: kvq.lib().kvq_ragged_attn_workspace_bytes(n, fmt, C.byref(d))  # noqa: E731
     assert size(0) == size(-1) == size(4, 6) == size(4, 99) == size(4, 1, kvq.dims(64, 2, 6, 128, 8)) == 0
-    sizes = [size(n) for n in (1, 2, 16, 64, 65, 100000)]
-    assert sizes == sorted(sizes) and sizes[0] > 0 and sizes[-1] == sizes[-3]   # grows up to a block's 256 rows
+    sizes = [size(n) for n in (1, 2, 16, 64, 65, 256, 257, 100000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0 and sizes[-1] == sizes[-3]   # grows up to 256 tokens
 
 
 # ------------------------------------------------------------------ the binding
