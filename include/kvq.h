@@ -507,18 +507,30 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
  * cu_q     device, [n_seqs + 1] int32, non-decreasing within [0, total_q]. A
  *          sequence whose range is not so is skipped and sets KVQ_DEVERR_RANGE.
  * out      device, [total_q][n_q_heads][head_dim], contiguous, BF16 or FP32 per
- *          out_dtype; not overlapping q (KVQ_ERR_ARG). BF16: the softmax
- *          weights enter the second product rounded to 11 bits (8 for a BF16
- *          cache); FP32: to 22 (16) bits.
+ *          out_dtype; not overlapping q (KVQ_ERR_ARG).
  * window   0: none.
- * workspace  at least kvq_ragged_attn_workspace_bytes(...) bytes, contents on
- *          entry do not matter (0 from that call: invalid arguments).
+ * workspace  at least kvq_ragged_attn_workspace_bytes(total_q, ...) bytes (a size
+ *          that does not fall with total_q), 16-byte aligned; contents on entry do
+ *          not matter. One call at a time uses it: calls, or replays of captured
+ *          graphs, that may run at the same time need one each.
  * The other arguments are those of kvq_decode_attn. A context that is not legal
  * (KVQ_DEVERR_CONTEXT) counts as empty: its rows are zeros. A token on a block
- * id outside the pool (KVQ_DEVERR_BLOCK) is not attended. A NaN or an infinity
- * in a V row (with a per-token scale: a scale that is one) makes the rows that
- * attend that token not finite, in its channels or in all of them, and no other
- * row.
+ * id outside the pool (KVQ_DEVERR_BLOCK) is not attended.
+ *
+ * Roundings. Sums, maxima and the softmax's sum are FP32. BF16 output: the
+ * values code * scale and the softmax weights enter the products rounded to 11
+ * bits (BF16 cache: values as stored, weights 8 bits); a token's V keeps them
+ * while its scale is above 2^-21 of the largest scale of the 64 tokens around it
+ * (E5M2: 2^-14). FP32 output: the codes and scales are exact, the weights have 22
+ * (BF16 cache: 24) bits. Sequences with one new token may be served by the
+ * kernels of kvq_decode_attn, with their roundings (weights of at least 18 bits;
+ * INT8: 24 bits of fixed point below the largest weight times the largest scale
+ * of 128 tokens), in calls without a window.
+ *
+ * A NaN or an infinity in a V row (with a per-token scale: a scale that is one)
+ * makes the rows that attend that token not finite, in its channels or in all of
+ * them, and no other row; with an INT8 cache, a sequence with one new token may
+ * come out finite as kvq_decode_attn does.
  * No length is needed on the host: a captured graph may be replayed with other
  * cu_q and context_lens of at most n_seqs sequences and total_q tokens.
  */

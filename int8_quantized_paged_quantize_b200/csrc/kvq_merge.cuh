@@ -43,6 +43,12 @@ __global__ void __launch_bounds__(128) merge_kernel(const int32_t* __restrict__ 
   tc::grid_dep_wait();                                     // the partials are complete
   if (bq >= rows) return;
   const int b = bq / Hq;
+  int64_t row = bq;
+  if (dst_row) {                                           // sequence b's rows go elsewhere, or nowhere
+    const int to = dst_row[b];
+    if (to < 0) return;
+    row = int64_t(to) * Hq + bq % Hq;
+  }
   const int64_t r0 = int64_t(bq) * slots;
   // The length, the count, the first 32 slots' (m, l) and the first PRE slots'
   // vectors are requested together, before the count is known (every slot
@@ -112,12 +118,6 @@ __global__ void __launch_bounds__(128) merge_kernel(const int32_t* __restrict__ 
   float r[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = l != 0.f ? o[i] / l : 0.f;
-  int64_t row = bq;
-  if (dst_row) {                                           // sequence b's rows go elsewhere, or nowhere
-    const int to = dst_row[b];
-    if (to < 0) return;
-    row = int64_t(to) * Hq + bq % Hq;
-  }
   OutT* dst = out + row * D + lane * N;
   if constexpr (sizeof(OutT) == 4) {
     if constexpr (N == 4) *reinterpret_cast<float4*>(dst) = make_float4(r[0], r[1], r[2], r[3]);

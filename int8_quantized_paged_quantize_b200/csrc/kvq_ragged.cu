@@ -24,17 +24,24 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// A call with one new token a sequence and no window is a decode step: its single
-// tokens go through the decode kernels, which multiply the codes as they are stored (64
-// sequences of 1,024 to 8,192 tokens, 32/8 heads, FP8: 100 us against 270 us of the
-// ragged kernel, whose converters and producer take 1,800 cycles a step however few
-// rows there are; 3 of up to 8,192, 8 KV heads: 22 against 38 us; 1 of 100, 1 KV head: 14
-// against 14 us). Not with FP8 and FP32 output, where their weights would have 18 bits
-// instead of 22; nor with contexts above kRtLong for each (sequence, KV head), of which
-// the decode kernels' at most 15 splits leave SMs idle (1 of 60,000 tokens, 1 KV head: 56
-// against 47 us).
+// Single new tokens, in a call without a window, can go through the decode kernels, which
+// multiply the codes as they are stored: the ragged kernel's converters and producer take
+// 1,800 cycles a step of 64 tokens however few rows there are. The lengths are on the
+// device, so the choice is by the call's shape; the ragged kernel always runs, leaves the
+// single tokens out and hands their rows on.
+//   total_q = n_seqs, a decode step: always (32/8 heads; 64 sequences of 1,024 to 8,192
+//     tokens: FP8 99 against 270 us, INT8 98 / 327, BF16 177 / 216; 8 of up to 256: 16 / 24;
+//     1 of 100: 14 / 20);
+//   total_q > n_seqs, single tokens perhaps beside chunks: 8-bit caches from kRtWork
+//     (sequence, KV head, token)s on. FP8, 63 single tokens and a chunk of 512 at up to
+//     8,000 tokens: 171 / 343 us, 15 and 450 at up to 4,096: 87 / 96, 3 and 500 at 12,000: 140
+//     / 198; two empty launches where no sequence has one token: 8 chunks of 200 181 / 171, 4
+//     of 1,000 507 / 497, 16 of 30 79 / 67. BF16: 244 / 267, 83 / 78, 137 / 139: not worth it.
+// Not with FP8 and FP32 output, where their weights would have 18 bits instead of 22; nor
+// with contexts above kRtLong for each (sequence, KV head), of which the decode kernels' at
+// most 15 splits leave SMs idle (1 of 60,000 tokens, 1 KV head: 56 / 47 us).
 constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
-constexpr int64_t kRtLong = 32768;
+constexpr int64_t kRtLong = 32768, kRtWork = 1 << 18;
 
 // The decode kernels' plan: at most kRtSlots partials a row (the automatic plan's
 // number), and kRtRows of them over all sequences.
@@ -119,7 +126,8 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d,
   b.ctx1 = b.row1 = nullptr;
   b.q1 = nullptr;
   DecodePlan plan;
-  const bool step = !(HP && C::F8) && a.window == 0 && a.total_q == a.n_seqs && a.n_seqs <= kRtSeqs &&
+  const bool step = !(HP && C::F8) && a.window == 0 && a.n_seqs <= kRtSeqs &&
+                    (a.total_q == a.n_seqs || (!C::BF && a.total_q > a.n_seqs && int64_t(a.n_seqs) * d.n_kv_heads * a.max_ctx >= kRtWork)) &&
                     a.max_ctx <= kRtLong * a.n_seqs * d.n_kv_heads && rt_plan(a.n_seqs, a.max_ctx, d, &plan) == KVQ_OK &&
                     plan.total <= rt_bytes(a.n_seqs, d);
   char* at = ws + w.o + w.ml + w.pieces;

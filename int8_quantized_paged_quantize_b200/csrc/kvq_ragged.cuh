@@ -26,7 +26,7 @@
 //   FP32 output (HP): the codes of K stay as they are, and the scores take the
 //     token's K scale in FP32 and so are those of the dequantized cache. The V
 //     scale is parted: its power of two goes into the expanded V (exactly), its
-//     mantissa into P, which is kept to 22 (16) bits as two parts.
+//     mantissa into P, which is kept to 22 bits as two parts (BF16 cache: 24, three).
 // With static INT8 scales the K scale of each channel multiplies the query (HP:
 // kept as two f16 parts) and the V scale the finished channel.
 //
@@ -93,8 +93,11 @@ struct RgCfg {
   static constexpr int METAB = kBlockSize * MV * 2;              // raw scale bytes of a page
   static constexpr int ST = kRgStep, PPS = kRgStep / kBlockSize; // tokens, pages per step
   static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
-  static constexpr int RPB = QP == 2 ? 128 : 256;                // rows per block
-  static constexpr int PP = HP ? 2 : 1;                          // weight parts
+  // weight parts. The third one has the columns of the slot's S, which its softmax warps have
+  // read by then; a block of at most 128 rows issues a slot's next scores behind its values.
+  // (That also halves the products that a slot adds up: the tensor cores round sums down.)
+  static constexpr int PP = HP ? (BF ? 3 : 2) : 1;
+  static constexpr int RPB = QP == 2 || PP == 3 ? 128 : 256;     // rows per block
   // The largest scale of a step is expanded to up to 2^UP, which its codes (448, 255 less
   // the zero point, 57344) leave room for below 65504. BF16 output: a token keeps its 11
   // bits while its scale is above 2^-(14 + UP) of the step's largest
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           for (int j = 0; j < C::PP; ++j)
 #pragma unroll
             for (int kk = 0; kk < C::PPS; ++kk)
-              rg_mma_ts<rg_desc_hi<C::V_SBO>()>(od, pa + j * 32 + 8 * kk, vb + kk * (C::CPAGE / 16), id_pv,
+              rg_mma_ts<rg_desc_hi<C::V_SBO>()>(od, (j < 2 ? pa + j * 32 : tmem + C::COL_S + x * 64) + 8 * kk, vb + kk * (C::CPAGE / 16), id_pv,
                                                 (j | kk) ? 1u : uint32_t(!first));
           mma_commit(pvdone + x);
           if (frees) mma_commit(C::BF ? rfree + stage : cfree + stage);   // the step's last product
@@ -1194,7 +1197,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       if (narrow) {
         const uint32_t z[16] = {};
 #pragma unroll
-        for (int c = 0; c < 2 * C::PP; ++c) tmem_st16(t_p + 16 * c, z);
+        for (int c = 0; c < (C::PP > 1 ? 4 : 2); ++c) tmem_st16(t_p + 16 * c, z);
         tmem_st_wait();
       }
       // operand stage, and its phase, of this slot's first step
@@ -1316,7 +1319,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 #pragma unroll
           for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = make_float2(ex2_ftz(x2[k].x), ex2_ftz(x2[k].y));
         };
-        uint32_t ph[16], pl[16];
+        uint32_t ph[16], pl[16], pt[16];
         float4 fs[4];
         expo(0);
 #pragma unroll
@@ -1338,17 +1341,19 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             if constexpr (C::BF) {
               const __nv_bfloat162 b16 = __floats2bfloat162_rn(wv.x, wv.y);
               ph[o] = *reinterpret_cast<const uint32_t*>(&b16);
-              if constexpr (C::PP == 2) hv = make_float2(bf16_lo(ph[o]), bf16_hi(ph[o]));
+              if constexpr (C::PP >= 2) hv = make_float2(bf16_lo(ph[o]), bf16_hi(ph[o]));
             } else {
               const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
               ph[o] = *reinterpret_cast<const uint32_t*>(&f16);
               if constexpr (C::PP == 2) hv = __half22float2(f16);
             }
-            if constexpr (C::PP == 2) {
+            if constexpr (C::PP >= 2) {
               const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
               if constexpr (C::BF) {
                 const __nv_bfloat162 b16 = __floats2bfloat162_rn(rest.x, rest.y);
                 pl[o] = *reinterpret_cast<const uint32_t*>(&b16);
+                const __nv_bfloat162 t16 = __floats2bfloat162_rn(rest.x - bf16_lo(pl[o]), rest.y - bf16_hi(pl[o]));
+                pt[o] = *reinterpret_cast<const uint32_t*>(&t16);
               } else {
                 const __half2 f16 = __floats2half2_rn(rest.x, rest.y);
                 pl[o] = *reinterpret_cast<const uint32_t*>(&f16);
@@ -1363,10 +1368,18 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             }
             if constexpr (NCH == 1) {
               tmem_st8(t_p + col0 / 2, ph);
-              if constexpr (C::PP == 2) tmem_st8(t_p + 32 + col0 / 2, pl);
+              if constexpr (C::PP >= 2) tmem_st8(t_p + 32 + col0 / 2, pl);
+              if constexpr (C::PP == 3) {
+                const uint32_t z[8] = {};                  // S was in the other warps' columns
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  if (w != quarter) tmem_st8(t_s + 8 * w, z);
+                tmem_st8(t_s + col0 / 2, pt);
+              }
             } else {
               tmem_st16(t_p + 8 * (c - 1), ph);
-              if constexpr (C::PP == 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
+              if constexpr (C::PP >= 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
+              if constexpr (C::PP == 3) tmem_st16(t_s + 8 * (c - 1), pt);
             }
           }
         }

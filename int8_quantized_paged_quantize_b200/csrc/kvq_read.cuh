@@ -5,8 +5,7 @@
 // finds their sequences, and walks them in segments (consecutive tokens of one
 // page). Of a segment's K page a lane holds 16 channels of a token, as the
 // page stores them, and writes them as one 32-byte piece. The V page is
-// transposed, so it passes through shared memory (or, for the packed low-bit
-// pages, comes as it is): a lane takes 4 tokens x 16 channels and turns them by
+// transposed, so it passes through shared memory: a lane takes 4 tokens x 16 channels and turns them by
 // byte permutes, with the chunks placed so that the 8 channel groups read
 // different banks. Nothing is computed in fewer than 32 bits; the values are
 // rounded once, to the output type.
@@ -27,8 +26,10 @@ struct ReadCfg {
   static constexpr int BITS = FMT == KVQ_KIVI2 ? 2 : FMT == KVQ_KIVI4 ? 4 : FMT == KVQ_BF16 ? 16 : 8;
   static constexpr int PAGE = kBlockSize * D * BITS / 8;
   static constexpr int WARPS = 8;
-  // the V page of a warp (the low-bit pages need no transposition)
-  static constexpr int SMEM = KIVI ? 16 : PAGE;
+  // the V page of a warp; low-bit pages: 16 bytes apart after every 16 channels, so that
+  // the 8 channel groups of a warp's reads lie in different banks
+  static constexpr int GROUPB = 4 * BITS * 8;                    // bytes of 16 channels of a V page
+  static constexpr int SMEM = KIVI ? PAGE + (D / 16) * 16 : PAGE;
 };
 
 // 16 output values as one row piece.
@@ -86,8 +87,11 @@ __device__ __forceinline__ int warp_upper(const int32_t* cu, int n, int r, int l
   return lo;
 }
 
+// 3 CTAs an SM (80 registers; BF16 pages: 2): 32 whole contexts of 4,100 tokens, 8 KV heads,
+// INT8 167 us against 198 at 128 registers and 212 with K and V in CTAs of their own; 4-bit
+// 57 against 66. At 4 the spills cost more.
 template <int D, int FMT, typename OutT>
-__global__ void __launch_bounds__(256) read_kernel(
+__global__ void __launch_bounds__(256, FMT == KVQ_BF16 ? 2 : 3) read_kernel(
     const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
     const __nv_bfloat16* __restrict__ ks, const __nv_bfloat16* __restrict__ vs,
     const int32_t* __restrict__ tables, const int32_t* __restrict__ starts,
@@ -170,13 +174,12 @@ __global__ void __launch_bounds__(256) read_kernel(
     const uint8_t* vp = vc + page * C::PAGE;
 
     // ---- V: its loads first, so that they are in flight under K's
-    constexpr int VL = C::KIVI ? 1 : C::PAGE / 512;
+    constexpr int VL = (C::PAGE + 511) / 512;     // 2 bits at D = 64: half a warp's chunks
     uint4 vraw[VL];
-    if constexpr (!C::KIVI) {
-      if (vo) {
+    if (vo) {
 #pragma unroll
-        for (int i = 0; i < VL; ++i) vraw[i] = reinterpret_cast<const uint4*>(vp)[lane + 32 * i];
-      }
+      for (int i = 0; i < VL; ++i)
+        if (C::PAGE >= 512 * (i + 1) || (lane + 32 * i) * 16 < C::PAGE) vraw[i] = reinterpret_cast<const uint4*>(vp)[lane + 32 * i];
     }
 
     // ---- K: item j = (token group, piece c, token): 16 channels of a token
@@ -253,14 +256,14 @@ __global__ void __launch_bounds__(256) read_kernel(
               mb = -1;
             }
 #pragma unroll
-            for (int e = 0; e < (PER < 16 ? PER : 16); ++e) {
-              float s = 0.f, z = 0.f;
-              if (mb >= 0) {
-                const __nv_bfloat162 m = reinterpret_cast<const __nv_bfloat162*>(ks)[(int64_t(mb) * Hk + h) * kBlockSize + (ch % PER) + e];
-                s = __low2float(m);
-                z = __high2float(m);
-              }
-              x[e0 + e] = __fmaf_rn(x[e0 + e], s, z);
+            for (int e = 0; e < (PER < 16 ? PER : 16); e += 4) {   // four (s, z) pairs
+              uint4 m = make_uint4(0, 0, 0, 0);
+              if (mb >= 0)
+                m = __ldg(reinterpret_cast<const uint4*>(ks + ((int64_t(mb) * Hk + h) * kBlockSize + ch % PER + e) * 2));
+              x[e0 + e] = __fmaf_rn(x[e0 + e], bf16_lo(m.x), bf16_hi(m.x));
+              x[e0 + e + 1] = __fmaf_rn(x[e0 + e + 1], bf16_lo(m.y), bf16_hi(m.y));
+              x[e0 + e + 2] = __fmaf_rn(x[e0 + e + 2], bf16_lo(m.z), bf16_hi(m.z));
+              x[e0 + e + 3] = __fmaf_rn(x[e0 + e + 3], bf16_lo(m.w), bf16_hi(m.w));
             }
           }
         }
@@ -273,16 +276,22 @@ __global__ void __launch_bounds__(256) read_kernel(
       const int g = lane & 7, tq = lane >> 3;
       uint32_t cw[16];                            // codes: 4 tokens of channel 16 g + i (8 bits each)
       uint32_t cw2[C::BITS == 16 ? 16 : 1];       // BF16: tokens 4 tq, +1 in cw, +2, +3 in cw2
-      if constexpr (!C::KIVI) {
+      __syncwarp();
+      if constexpr (C::KIVI) {
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          const int at = (lane + 32 * i) * 16;
+          if (at < C::PAGE) *reinterpret_cast<uint4*>(smem[warp] + at + at / C::GROUPB * 16) = vraw[i];
+        }
+      } else {
         // chunk x (channel x % D) at x with its low 3 bits xored by the piece
-        __syncwarp();
 #pragma unroll
         for (int i = 0; i < VL; ++i) {
           const int xch = lane + 32 * i;
           *reinterpret_cast<uint4*>(smem[warp] + (xch ^ ((xch >> 4) & 7)) * 16) = vraw[i];
         }
-        __syncwarp();
       }
+      __syncwarp();
       if (g < NCH && 4 * tq < o0 + len && 4 * tq + 4 > o0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -295,10 +304,10 @@ __global__ void __launch_bounds__(256) read_kernel(
           } else if constexpr (C::BITS == 8) {
             cw[i] = *reinterpret_cast<const uint32_t*>(smem[warp] + (ch ^ ((ch >> 4) & 7)) * 16 + tq * 4);
           } else if constexpr (C::BITS == 4) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(vp)[2 * ch + (tq >> 1)];
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(smem[warp] + 8 * ch + 16 * g + 4 * (tq >> 1));
             cw[i] = (w >> (4 * (tq & 1))) & 0x0f0f0f0fu;
           } else {
-            cw[i] = (reinterpret_cast<const uint32_t*>(vp)[ch] >> (2 * tq)) & 0x03030303u;
+            cw[i] = (*reinterpret_cast<const uint32_t*>(smem[warp] + 4 * ch + 16 * g) >> (2 * tq)) & 0x03030303u;
           }
         }
 #pragma unroll
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(256) read_kernel(
           store16(vo + ((row0 + t - o0) * Hk + h) * D + 16 * g, x, wide);
         }
       }
-      if constexpr (!C::KIVI) __syncwarp();
+      __syncwarp();
     }
   }
 }

@@ -526,7 +526,8 @@ def ragged_attn(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables, conte
     (kvq_ragged_attn). q: [T][Hq][D] bf16 (a strided view will do), the new tokens
     of all sequences one after another, cu_q [B + 1] int32 where each begins; they
     are the last tokens of the sequences' contexts, already appended. out:
-    [T][Hq][D] bf16 or float32 (None: allocated, of out_dtype); returned."""
+    [T][Hq][D] bf16 or float32 (None: allocated, of out_dtype); returned. A workspace
+    serves one call at a time."""
     dev, ctx = _launch_on(q, stream, "q")
     return _within(ctx, _ragged_attn, dev, q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
                    context_lens, max_context_len, sm_scale, out, fmt, d, window, workspace, out_dtype)
@@ -552,7 +553,7 @@ def _ragged_attn(dev, q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
     rc = lib().kvq_ragged_attn(qp, qs, _at(dev, cu_q, _I32, "cu_q", (B + 1,)), B, T, kc, vc, _PAIR(ks, vs),
                                _at(dev, block_tables, _I32, "block_tables", (B, d.max_blocks_per_seq)),
                                _at(dev, context_lens, _I32, "context_lens", (B,)), int(max_context_len),
-                               int(window), sm_scale, op, 0 if dt is _BF16 else 1, workspace.data_ptr(),
+                               min(int(window), 2 ** 31 - 1), sm_scale, op, 0 if dt is _BF16 else 1, workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), FMT[fmt], ctypes.byref(d),
                                _raw_stream(dev))
     if rc:

@@ -88,7 +88,7 @@ def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32, step=False):
                cache is exact. In both: 2^-13 of the products' sum for sums of up to
                128 terms, kept to at least 20 bits.
       weights  half a step of f16 (BF16 cache: of bf16): 2^-11 (2^-8); FP32 output
-               twice that many bits: 2^-22 (2^-16). 2^-20 for the exponential and the sum.
+               twice that many bits, 2^-22 (BF16 cache: 2^-22 and more). 2^-20 for the exponential and the sum.
       V        BF16 output with per-token scales: 2^-11.
       output   half a step of bf16 2^-8, or of FP32.
     A score off by at most d moves a weight by a factor of at most e^(2d).
@@ -113,7 +113,7 @@ def attention_and_bound(q, cu, kv, sm_scale, Hk, window, fmt, f32, step=False):
     out, bound = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
     tok = fmt in ("fp8", "e5m2", "int8")
     ds = 2.0 ** -18 + (0.0 if f32 or fmt == "bf16" else 2.0 ** -11)
-    dp = (2.0 ** -16 if f32 else 2.0 ** -8) if fmt == "bf16" else (2.0 ** -22 if f32 else 2.0 ** -11)
+    dp = 2.0 ** -22 if f32 else 2.0 ** (-8 if fmt == "bf16" else -11)
     dv = 2.0 ** -11 if tok and not f32 else 0.0
     do = 2.0 ** -23 if f32 else 2.0 ** -8
     for b, (K, V) in enumerate(kv):

@@ -261,10 +261,13 @@ def test_decode_steps(fmt, D, G):
     q = query(rng, B, f)
     mixed = [1] * B
     mixed[0], mixed[1], mixed[2], mixed[7], mixed[8], mixed[B - 1] = 0, 2, 0, 0, 3, 0
-    for n in ([1] * B, mixed):
+    more = [1] * B                                   # more tokens than sequences: chunks beside single tokens
+    more[5], more[9], more[11], more[B - 1] = 37, 0, 2, 9
+    q = query(rng, sum(more), f)
+    for n in ([1] * B, mixed, more):
         m = sum(n)
         for f32 in (False, True):
-            out = step_call(f, n, q, out_dtype=torch.float32 if f32 else torch.bfloat16)
+            out = step_call(f, n, q[:m], out_dtype=torch.float32 if f32 else torch.bfloat16)
             assert kvq.device_error() == 0
             ref, bound = SC.attention_and_bound(q[:m], np.concatenate([[0], np.cumsum(n)]), f.kv(), D ** -0.5, f.Hk, 0, fmt, f32)
             SC.assert_within(out[:m], ref, bound)
