@@ -7,6 +7,10 @@ Two hot operations, both hand-written CUDA for sm_100a behind the C-ABI library
 * ``decode_attn`` paged GQA decode attention that dequantises the cache in
                   registers, with an online-softmax split-K and a merge kernel.
 
+and the calls of a serving step: ``append_rope`` (rotary embedding and append in
+one), ``ragged_attn`` (ragged chunks of new tokens over the paged cache), ``read``
+(dequantizing read-back).
+
 The Python layer (``kvq``) only marshals arguments: PyTorch tensors supply device
 pointers and the current CUDA stream. Nothing here computes on the CPU; if the
 library is missing, every call raises.
