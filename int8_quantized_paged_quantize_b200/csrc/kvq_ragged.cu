@@ -57,11 +57,12 @@ size_t rt_bytes(int32_t n, const kvq_dims& d) {
          round256(size_t(n) * d.n_q_heads * sizeof(int32_t));
 }
 
-// Workspace pieces: two places per CTA of `rows` rows each; for a decode step each
+// Workspace pieces: two places per CTA of `rows` rows each; the sums of its two slots (FP32
+// output); for a decode step each
 // sequence's context and output row, its query and the decode kernels' workspace.
 struct RgSpace {
   int rows;
-  size_t o, ml, pieces, seqs, q1, total;
+  size_t o, ml, pieces, sums, seqs, q1, total;
 };
 RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   RgSpace w;
@@ -71,7 +72,8 @@ RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   w.o = round256(places * w.rows * d.head_dim * sizeof(float));
   w.ml = round256(places * w.rows * 2 * sizeof(float));
   w.pieces = round256(places * sizeof(RgPiece));
-  w.total = w.o + w.ml + w.pieces;
+  w.sums = round256(places * 128 * d.head_dim * sizeof(float));
+  w.total = w.o + w.ml + w.pieces + w.sums;
   const int32_t n = std::min(total_q, kRtSeqs);
   w.seqs = round256(size_t(n) * sizeof(int32_t));
   w.q1 = round256(size_t(n) * d.n_q_heads * d.head_dim * 2);
@@ -130,7 +132,8 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d,
                     (a.total_q == a.n_seqs || (!C::BF && a.total_q > a.n_seqs && int64_t(a.n_seqs) * d.n_kv_heads * a.max_ctx >= kRtWork)) &&
                     a.max_ctx <= kRtLong * a.n_seqs * d.n_kv_heads && rt_plan(a.n_seqs, a.max_ctx, d, &plan) == KVQ_OK &&
                     plan.total <= rt_bytes(a.n_seqs, d);
-  char* at = ws + w.o + w.ml + w.pieces;
+  float* sums = reinterpret_cast<float*>(ws + w.o + w.ml + w.pieces);
+  char* at = ws + w.o + w.ml + w.pieces + w.sums;
   if (step) {
     b.ctx1 = reinterpret_cast<int32_t*>(at);
     b.row1 = reinterpret_cast<int32_t*>(at + w.seqs);
@@ -141,7 +144,7 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d,
                  static_cast<const __nv_bfloat16*>(a.q), a.q_stride, static_cast<const uint8_t*>(a.kc),
                  static_cast<const uint8_t*>(a.vc), static_cast<const __nv_bfloat16*>(a.ks),
                  static_cast<const __nv_bfloat16*>(a.vs), a.tables, b, int(d.num_blocks),
-                 a.sm_scale * kLog2e, per_tensor, decode_wait_limit(), a.out, po, pml, pieces, w.rows);
+                 a.sm_scale * kLog2e, per_tensor, decode_wait_limit(), a.out, po, pml, pieces, w.rows, sums);
   if (e != cudaSuccess) return e;
   e = launch_pdl(ragged_merge_kernel<D, OutT>, dim3(unsigned(grid), unsigned((std::min(w.rows, C::RPB) + 31) / 32)),
                  dim3(256), 0, st, static_cast<const float*>(po), static_cast<const float*>(pml),

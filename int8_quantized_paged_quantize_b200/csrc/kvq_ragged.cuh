@@ -79,6 +79,7 @@ namespace kvq {
 
 constexpr int kRgRing = 4;                     // pieces handed ahead
 constexpr int kRgGroup = 4;                    // steps of a group of the producer (4 pages a step, a lane each)
+constexpr int kRgFlush = 16;                   // steps of a slot that the tensor cores add up (FP32 output)
 constexpr int kRgNarrow = 16;                  // rows that every warp of a slot has a copy of
 
 template <int D, int FMT, bool HP>
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
     const uint8_t* __restrict__ vc, const __nv_bfloat16* __restrict__ ks,
     const __nv_bfloat16* __restrict__ vs, const int32_t* __restrict__ tables, const RgBatch bt, int NB,
     float qk_scale, int per_tensor, long long wait_limit, void* __restrict__ out_,
-    float* __restrict__ part_o, float* __restrict__ part_ml, RgPiece* __restrict__ pieces, int rows_cap) {
+    float* __restrict__ part_o, float* __restrict__ part_ml, RgPiece* __restrict__ pieces, int rows_cap,
+    float* __restrict__ sums) {
   using C = RgCfg<D, FMT, HP>;
   using namespace tc;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -714,24 +716,29 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         ok = wait(qready, par_q);
         par_q ^= 1u;
         int last = 0;                                      // the stage of the step before
+        // whether the values of step v are the first of their slot's O
+        auto first = [&](int v) -> bool {
+          const int k = two ? v : v >> 1;
+          return HP ? k % kRgFlush == 0 : k == 0;
+        };
         for (int i = 0; ok && i < steps; ++i) {
           ok = wait(cfull + stage, (par_c >> stage) & 1u);
           if (!ok) break;
           par_c ^= 1u << stage;
           if (two) {
             ok = scores(0, stage, 0);
-            if (ok && i > 0) ok = values(0, last, i == 1, false);
+            if (ok && i > 0) ok = values(0, last, first(i - 1), false);
             if (ok) ok = scores(1, stage, 1);
-            if (ok && i > 0) ok = values(1, last, i == 1, true);
+            if (ok && i > 0) ok = values(1, last, first(i - 1), true);
           } else {
             ok = scores(i & 1, stage, 0);
-            if (ok && i > 0) ok = values((i & 1) ^ 1, last, i <= 2, true);
+            if (ok && i > 0) ok = values((i & 1) ^ 1, last, first(i - 1), true);
           }
           last = stage;
           stage = stage + 1 == C::NC ? 0 : stage + 1;
         }
-        if (ok && two) ok = values(0, last, steps == 1, false) && values(1, last, steps == 1, true);
-        if (ok && !two) ok = values((steps - 1) & 1, last, steps <= 2, true);
+        if (ok && two) ok = values(0, last, first(steps - 1), false) && values(1, last, first(steps - 1), true);
+        if (ok && !two) ok = values((steps - 1) & 1, last, first(steps - 1), true);
       }
       // every product issued completes before tensor memory is released
       volatile int no_abort = 0;
@@ -1191,6 +1198,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       const int lim_min = __reduce_min_sync(0xffffffffu, lim), lo_max = __reduce_max_sync(0xffffffffu, lo_t);
       float m_run = -INFINITY, mref = 0.f, l = 0.f;   // mref: m_run, or 0 where it is -inf
       bool any_step = false;
+      // FP32 output: the tensor cores round their sums down, by up to a last bit for each
+      // product added; so a slot's O goes to the workspace every kRgFlush steps (rows side by
+      // side, each thread its own) and is added up there in FP32. m_sum: their reference.
+      float* sum = sums + (int64_t(blockIdx.x) * 2 + x) * 128 * D + r;
+      float m_sum = -INFINITY;
+      bool summed = false;
       // A narrow block: all four warps of a slot have its rows, each for 16 of a
       // step's tokens, as a softmax of their own (P is zero in the others' columns).
       const bool narrow = pw.rows <= kRgNarrow;
@@ -1412,6 +1425,26 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           ++cnt;
           continue;
         }
+        if (HP && (two ? i : i >> 1) % kRgFlush == 0 && any_step) {
+          wait_all(pvdone + x, (cnt - 1) & 1);
+          tc_fence_after();
+          const float f = ex2_ftz(m_sum - mref);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16(t_o + 16 * c, ov);
+            float was[16] = {};
+            if (summed) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) was[e] = sum[(16 * c + e) * 128] * f;
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[(16 * c + e) * 128] = was[e] + __uint_as_float(ov[e]);
+          }
+          m_sum = m_run;
+          summed = true;
+        }
         if (narrow) softmax_step(std::integral_constant<int, 16>{}, i, ck);
         else softmax_step(std::integral_constant<int, C::ST>{}, i, ck);
         ++cnt;
@@ -1434,6 +1467,16 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // ---- the piece's end: O of the last step
       if (any_step) wait_all(pvdone + x, (cnt - 1) & 1);
       tc_fence_after();
+      const float f_sum = HP && summed ? ex2_ftz(m_sum - mref) : 0.f;
+      auto add_sums = [&](uint32_t (&ov)[16], int c) {
+        if constexpr (HP) {
+          if (summed) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              ov[e] = __float_as_uint(__uint_as_float(ov[e]) + sum[(16 * c + e) * 128] * f_sum);
+          }
+        }
+      };
       const bool whole = pw.lo == 0 && pw.hi == pw.count;
       const int64_t place = int64_t(blockIdx.x) * 2 + (pw.lo == 0 ? 1 : 0);
       auto out_row = [&](int row) -> int64_t {
@@ -1467,6 +1510,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           uint32_t ov[16];
           tmem_ld16(t_o + 16 * c, ov);
           tmem_ld_wait();
+          add_sums(ov, c);
           if (lane < kRgNarrow) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -1511,6 +1555,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           uint32_t ov[16];
           tmem_ld16(t_o + 16 * c, ov);
           tmem_ld_wait();
+          add_sums(ov, c);
           float o[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = any_step ? __uint_as_float(ov[e]) : 0.f;

@@ -107,6 +107,32 @@ def test_one_long_sequence(fmt, f32):
         run(f, n, f32=f32)
 
 
+@pytest.mark.parametrize("fmt,n,G", [("int8", 200, 1), ("int8", 60, 1), ("fp8", 1, 4), ("bf16", 60, 2), ("int8c", 100, 1)])
+def test_long_pieces(fmt, n, G):
+    """Pieces of many steps in one CTA (sequences that share their blocks, so many that the
+    shares hold whole blocks), whose FP32 sums pass through the workspace."""
+    B, L = 40, 2900
+    f = SC.Filled(fmt, [L], Hk=8, G=G, D=64)
+    rng = np.random.default_rng(n)
+    rows = [n] * B + ([2] if n == 1 else [])         # not a decode step
+    q = query(rng, sum(rows), f)
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    tables = f.d_tables.expand(len(rows), -1).contiguous()
+    kv = f.kv() * len(rows)
+    for f32 in (True, False):
+        out = f.cache.ragged(SC.bf16(q).cuda(), SC.i32(cu), tables, SC.i32([L] * len(rows)), L, window=L - 1 if n == 1 else 0,
+                             out_dtype=torch.float32 if f32 else torch.bfloat16)
+        assert kvq.device_error() == 0
+        for b in (0, 17, B - 1):                     # some of them, a few rows of each
+            pick = [0] if n == 1 else [0, n // 2, n - 1]
+            for i in pick:
+                p = L - rows[b] + i
+                lo = max(0, p - (L - 1) + 1) if n == 1 else 0
+                one = [(kv[b][0][lo:p + 1], kv[b][1][lo:p + 1])]
+                ref, bound = SC.attention_and_bound(q[cu[b] + i:cu[b] + i + 1], [0, 1], one, f.D ** -0.5, 8, 0, fmt, f32)
+                SC.assert_within(out[cu[b] + i:cu[b] + i + 1], ref, bound, note=(fmt, n, b, i, f32))
+
+
 def test_many_sequences():
     """More sequences than threads of a CTA; most without new tokens, or contexts."""
     rng = np.random.default_rng(0)
