@@ -521,11 +521,12 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
  * values code * scale and the softmax weights enter the products rounded to 11
  * bits (BF16 cache: values as stored, weights 8 bits); a token's V keeps them
  * while its scale is above 2^-21 of the largest scale of the 64 tokens around it
- * (E5M2: 2^-14). FP32 output: the codes and scales are exact, the weights have 22
- * (BF16 cache: 24) bits. Sequences with one new token may be served by the
- * kernels of kvq_decode_attn, with their roundings (weights of at least 18 bits;
- * INT8: 24 bits of fixed point below the largest weight times the largest scale
- * of 128 tokens), in calls without a window.
+ * (E5M2: 2^-14). FP32 output: the codes and scales are exact, the weights have 24
+ * bits, however far below the largest one they lie. With BF16 output, or a BF16
+ * cache, sequences with one new token may be served by the kernels of
+ * kvq_decode_attn, with their roundings (weights of at least 18 bits; INT8: 24
+ * bits of fixed point below the largest weight times the largest scale of 128
+ * tokens), in calls without a window.
  *
  * A NaN or an infinity in a V row (with a per-token scale: a scale that is one)
  * makes the rows that attend that token not finite, in its channels or in all of

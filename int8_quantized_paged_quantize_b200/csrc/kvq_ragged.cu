@@ -37,8 +37,9 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 //     8,000 tokens: 171 / 343 us, 15 and 450 at up to 4,096: 87 / 96, 3 and 500 at 12,000: 140
 //     / 198; two empty launches where no sequence has one token: 8 chunks of 200 181 / 171, 4
 //     of 1,000 507 / 497, 16 of 30 79 / 67. BF16: 244 / 267, 83 / 78, 137 / 139: not worth it.
-// Not with FP8 and FP32 output, where their weights would have 18 bits instead of 22; nor
-// with contexts above kRtLong for each (sequence, KV head), of which the decode kernels' at
+// Not with FP32 output over 8-bit caches: their weights have 18 bits (FP8), or 24 below the
+// largest one (INT8: tokens 12 nats below a dominant one came out 2e-3 off), the ragged
+// kernel's 24 of their own. Nor with contexts above kRtLong for each (sequence, KV head), of which the decode kernels' at
 // most 15 splits leave SMs idle (1 of 60,000 tokens, 1 KV head: 56 / 47 us).
 constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
 constexpr int64_t kRtLong = 32768, kRtWork = 1 << 18;
@@ -128,7 +129,7 @@ cudaError_t ragged_dispatch(const RaggedArgs& a, kvq_fmt fmt, const kvq_dims& d,
   b.ctx1 = b.row1 = nullptr;
   b.q1 = nullptr;
   DecodePlan plan;
-  const bool step = !(HP && C::F8) && a.window == 0 && a.n_seqs <= kRtSeqs &&
+  const bool step = !(HP && !C::BF) && a.window == 0 && a.n_seqs <= kRtSeqs &&
                     (a.total_q == a.n_seqs || (!C::BF && a.total_q > a.n_seqs && int64_t(a.n_seqs) * d.n_kv_heads * a.max_ctx >= kRtWork)) &&
                     a.max_ctx <= kRtLong * a.n_seqs * d.n_kv_heads && rt_plan(a.n_seqs, a.max_ctx, d, &plan) == KVQ_OK &&
                     plan.total <= rt_bytes(a.n_seqs, d);

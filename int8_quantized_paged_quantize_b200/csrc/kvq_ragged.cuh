@@ -24,9 +24,12 @@
 //     token: its 64 factors a step and thread, from shared memory, cost them as
 //     much as half of the exponentials.
 //   FP32 output (HP): the codes of K stay as they are, and the scores take the
-//     token's K scale in FP32 and so are those of the dequantized cache. The V
-//     scale is parted: its power of two goes into the expanded V (exactly), its
-//     mantissa into P, which is kept to 22 bits as two parts (BF16 cache: 24, three).
+//     token's K scale in FP32 and so are those of the dequantized cache. The codes
+//     of V, less their zero point, are exact in bf16, and P takes the token's V scale
+//     in FP32 and is kept to 24 bits as three bf16 parts. bf16 has the range of FP32, so
+//     a weight keeps its bits however far below the largest one it lies: as two f16
+//     parts, thousands of tokens 12 nats below a token without a value came out
+//     4e-3 off (1e-6 now), and 20 nats below it they were lost.
 // With static INT8 scales the K scale of each channel multiplies the query (HP:
 // kept as two f16 parts) and the V scale the finished channel.
 //
@@ -94,14 +97,17 @@ struct RgCfg {
   static constexpr int ST = kRgStep, PPS = kRgStep / kBlockSize; // tokens, pages per step
   static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
   // weight parts. The third one has the columns of the slot's S, which its softmax warps have
-  // read by then; a block of at most 128 rows issues a slot's next scores behind its values.
-  // (That also halves the products that a slot adds up: the tensor cores round sums down.)
-  static constexpr int PP = HP ? (BF ? 3 : 2) : 1;
+  // read by then; a slot's next scores are issued behind its values.
+  static constexpr int PP = HP ? 3 : 1;
+  static constexpr bool VB = BF || HP;                           // V operand and weights in bf16 (else f16)
   // FP32 output: steps of a slot that the tensor cores add up, before its O is added to FP32
-  // sums in the workspace. INT8, 1,024 rows at 4,096: 245 us without, 271 with 16 steps, 291
-  // with 8, 329 with 4; four chunks at 8,192 are off by 7e-6, 2.4e-6, 1.4e-6, 0.9e-6 (FP8)
-  static constexpr int FLUSH = BF ? 4 : 8;
-  static constexpr int RPB = QP == 2 || PP == 3 ? 128 : 256;     // rows per block
+  // sums in the workspace (a narrow block's warps have weights for 16 of a step's tokens each,
+  // a quarter of the additions). FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392
+  // with 4 (BF16 cache: 289, 307, 330); rows that see 8,192 tokens are off by 1.5e-6, 1.2e-6,
+  // 0.8e-6 (BF16 cache: 1.9e-6, 1.5e-6, 1.1e-6)
+  static constexpr int FLUSH = BF ? 4 : 6;
+  static __device__ __forceinline__ int flush(int rows) { return rows <= kRgNarrow ? 4 * FLUSH : FLUSH; }
+  static constexpr int RPB = QP == 2 ? 128 : 256;     // rows per block
   // The largest scale of a step is expanded to up to 2^UP, which its codes (448, 255 less
   // the zero point, 57344) leave room for below 65504. BF16 output: a token keeps its 11
   // bits while its scale is above 2^-(14 + UP) of the step's largest
@@ -110,7 +116,7 @@ struct RgCfg {
   static constexpr int NC = BF ? NRAW : 3;                       // operand stages
   static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
   static constexpr bool COLS = HP && MV > 0;                     // scores scaled token by token
-  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K scale, V mantissa per token; eV, 2^-eV, 2^eK of the step
+  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K and V scale per token; eV, 2^-eV, 2^eK of the step
   static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
@@ -304,6 +310,10 @@ __device__ __forceinline__ void sts_u4(uint32_t a, uint32_t x, uint32_t y, uint3
 __device__ __forceinline__ uint32_t rg_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return rg_pack(f.x, f.y);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -656,10 +666,13 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       //   two blocks of rows  S_A(i), O_A(i-1), S_B(i), O_B(i-1)
       //   one                 S_x(i), O_y(i-1)   (x, y the slots of the steps)
       // so that a slot's next scores are in the making while its softmax warps
-      // are still at work on the last ones.
+      // are still at work on the last ones. With three weight parts S has to wait
+      // for O, which reads the third from S's columns:
+      //   two blocks of rows  O_A(i-1), S_A(i), O_B(i-1), S_B(i)
+      // and a slot's softmax overlaps the other slot's products only.
       if (elect_one()) {
       constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
-      constexpr uint32_t id_pv = idesc_f16(D, C::BF);
+      constexpr uint32_t id_pv = idesc_f16(D, C::VB);
       // operand stages: K pages, then V pages
       const uint32_t q_lo = rg_desc_lo<C::Q_LBO>(smem_u32(qop));
       const uint32_t k_lo = rg_desc_lo<C::K_LBO>(smem_u32(C::BF ? raw : cst));
@@ -722,13 +735,18 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         // whether the values of step v are the first of their slot's O
         auto first = [&](int v) -> bool {
           const int k = two ? v : v >> 1;
-          return HP ? k % C::FLUSH == 0 : k == 0;
+          return HP ? k % C::flush(w.rows) == 0 : k == 0;
         };
         for (int i = 0; ok && i < steps; ++i) {
           ok = wait(cfull + stage, (par_c >> stage) & 1u);
           if (!ok) break;
           par_c ^= 1u << stage;
-          if (two) {
+          if (two && C::PP == 3) {
+            if (i > 0) ok = values(0, last, first(i - 1), false);
+            if (ok) ok = scores(0, stage, 0);
+            if (ok && i > 0) ok = values(1, last, first(i - 1), true);
+            if (ok) ok = scores(1, stage, 1);
+          } else if (two) {
             ok = scores(0, stage, 0);
             if (ok && i > 0) ok = values(0, last, first(i - 1), false);
             if (ok) ok = scores(1, stage, 1);
@@ -873,12 +891,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;   // tokens of the page that count
             // f16 pairs of neighbouring tokens' V factors and zero points; K factor and
             // zero point of token `lane % 16`, twice
-            uint32_t vf[C::MV > 0 ? 8 : 1], vz[C::ZP ? 8 : 1];
+            uint32_t vf[C::MV > 0 && !C::VB ? 8 : 1], vz[C::ZP ? 8 : 1];
             uint32_t kf = 0u, kz = 0u;
             if constexpr (C::MV > 0) {
-              // 2^(e + UP) above the step's largest finite scale
+              // the step's largest finite scale: 2^(e + UP) is above it
               constexpr int MB = 2 * C::MV;
-              auto top_of = [&](const uint8_t* m) -> int {
+              auto top_of = [&](const uint8_t* m) -> uint32_t {
                 uint32_t top = 0u;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
@@ -887,12 +905,24 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(m + t * MB);
                   if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);   // scales are not negative
                 }
-                top = __reduce_max_sync(0xffffffffu, top);
-                // no scale at all (or tiny ones): 2^-100, which leaves the reference to the
-                // steps whose V counts and keeps the sums of 2^(s - m) finite
+                return __reduce_max_sync(0xffffffffu, top);
+              };
+              // no scale at all (or tiny ones): 2^-100, which leaves the reference to the
+              // steps whose V counts and keeps the sums of 2^(s - m) finite
+              auto exponent = [](uint32_t top) -> int {
                 return top == 0u ? -100 : max(-100, min(126, int(top >> 7) - 126 - C::UP));
               };
-              const int ev = top_of(mv), ek = HP ? 0 : top_of(mk);
+              int ev, ek = 0;
+              const uint32_t vtop = top_of(mv);
+              if constexpr (HP) {
+                // a step's exponent is taken out of scales beyond 2^60 and 2^-60 only, so
+                // that weights times scales, and their sums, stay within FP32
+                const int e = int(vtop >> 7) - 127;
+                ev = vtop == 0u ? 0 : e > 60 ? e - 60 : e < -60 ? e + 60 : 0;
+              } else {
+                ev = exponent(vtop);
+                ek = exponent(top_of(mk));
+              }
               const float vdn = __int_as_float((127 - ev) << 23), kdn = __int_as_float((127 - ek) << 23);
               // this page's tokens: lane % 16
               const int t = 16 * pw + (lane & 15);
@@ -915,11 +945,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                 for (int j = 0; j < 8; ++j) out[j] = __shfl_sync(0xffffffffu, two, 2 * j);
               };
               if constexpr (HP) {
-                const int e = max(1, min(253, int(__float_as_uint(sv) >> 23)));   // sv >= 0 or NaN
-                pairs(wild ? sv : __int_as_float(e << 23) * vdn, vf);
                 if (lane < 16) {
                   cm[t] = sk * qk_scale;
-                  cm[C::ST + t] = wild ? 1.f : sv * __int_as_float((254 - e) << 23);
+                  cm[C::ST + t] = sv * vdn;
                 }
               } else {
                 pairs(sv * vdn, vf);
@@ -971,7 +999,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               if constexpr (C::ZP) codes16_less_pairs(codes, vz, o0, o1);
               else codes16_to_f16<FMT>(codes, o0, o1);
               uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-              if constexpr (C::MV > 0) {
+              if constexpr (C::VB) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wv[j] = f16x2_to_bf16x2(wv[j]);   // exact: codes less zero points
+              } else if constexpr (C::MV > 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) wv[j] = mul_f16x2(wv[j], vf[j]);
               }
@@ -1235,7 +1266,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        // HP: the tokens' K scales and V mantissas, four at a time; then {eV, 2^-eV, 2^eK}
+        // HP: the tokens' K and V scales, four at a time; then {eV, 2^-eV, 2^eK}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const int q0 = col0 / 4;
         const uint4 odd = cmask[3 * ck];
@@ -1323,8 +1354,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             tmem_st_wait();
           }
         }
-        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: times the mantissa of
-        // the token's V scale)
+        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: times the token's V scale
+        // 2^-eV)
         const float mx = ee.x - mref;
         const float2 dn2 = make_float2(f, f), nm2 = make_float2(mx, mx);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1335,7 +1366,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
 #pragma unroll
           for (int k = 8 * c; k < 8 * c + 8; ++k) x2[k] = make_float2(ex2_ftz(x2[k].x), ex2_ftz(x2[k].y));
         };
-        uint32_t ph[16], pl[16], pt[16];
+        constexpr int STC = C::PP == 3 || NCH == 1 ? 1 : 2;  // chunks stored together
+        uint32_t ph[8 * STC], pl[8 * STC], pt[8 * STC];
         float4 fs[4];
         expo(0);
 #pragma unroll
@@ -1347,38 +1379,29 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           if (c + 1 < NCH) expo(c + 1);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int kk = 8 * c + k, o = 8 * (c & 1) + k;
+            const int kk = 8 * c + k, o = 8 * (c % STC) + k;
             const float2 p2 = x2[kk];
             ls[k & 1] = __fadd2_rn(ls[k & 1], p2);
             float2 wv = p2;
             if constexpr (C::COLS)
               wv = __fmul2_rn(p2, (k & 1) ? make_float2(fs[k / 2].z, fs[k / 2].w) : make_float2(fs[k / 2].x, fs[k / 2].y));
             float2 hv;
-            if constexpr (C::BF) {
-              const __nv_bfloat162 b16 = __floats2bfloat162_rn(wv.x, wv.y);
-              ph[o] = *reinterpret_cast<const uint32_t*>(&b16);
+            if constexpr (C::VB) {
+              ph[o] = rg_pack(wv.x, wv.y);
               if constexpr (C::PP >= 2) hv = make_float2(bf16_lo(ph[o]), bf16_hi(ph[o]));
             } else {
               const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
               ph[o] = *reinterpret_cast<const uint32_t*>(&f16);
-              if constexpr (C::PP == 2) hv = __half22float2(f16);
             }
             if constexpr (C::PP >= 2) {
               const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
-              if constexpr (C::BF) {
-                const __nv_bfloat162 b16 = __floats2bfloat162_rn(rest.x, rest.y);
-                pl[o] = *reinterpret_cast<const uint32_t*>(&b16);
-                const __nv_bfloat162 t16 = __floats2bfloat162_rn(rest.x - bf16_lo(pl[o]), rest.y - bf16_hi(pl[o]));
-                pt[o] = *reinterpret_cast<const uint32_t*>(&t16);
-              } else {
-                const __half2 f16 = __floats2half2_rn(rest.x, rest.y);
-                pl[o] = *reinterpret_cast<const uint32_t*>(&f16);
-              }
+              pl[o] = rg_pack(rest.x, rest.y);
+              if constexpr (C::PP == 3) pt[o] = rg_pack(rest.x - bf16_lo(pl[o]), rest.y - bf16_hi(pl[o]));
             }
           }
-          if ((c & 1) || NCH == 1) {
+          if (c % STC == STC - 1) {
             // the last product has read P
-            if (c <= 1 && cnt > 0 && !pv_seen) {
+            if (c < STC && cnt > 0 && !pv_seen) {
               wait_all(pvdone + x, (cnt - 1) & 1);
               tc_fence_after();
             }
@@ -1392,10 +1415,13 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   if (w != quarter) tmem_st8(t_s + 8 * w, z);
                 tmem_st8(t_s + col0 / 2, pt);
               }
+            } else if constexpr (STC == 1) {
+              tmem_st8(t_p + 8 * c, ph);
+              tmem_st8(t_p + 32 + 8 * c, pl);
+              tmem_st8(t_s + 8 * c, pt);
             } else {
               tmem_st16(t_p + 8 * (c - 1), ph);
               if constexpr (C::PP >= 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
-              if constexpr (C::PP == 3) tmem_st16(t_s + 8 * (c - 1), pt);
             }
           }
         }
@@ -1428,7 +1454,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           ++cnt;
           continue;
         }
-        if (HP && (two ? i : i >> 1) % C::FLUSH == 0 && any_step) {
+        if (HP && (two ? i : i >> 1) % C::flush(pw.rows) == 0 && any_step) {
           wait_all(pvdone + x, (cnt - 1) & 1);
           tc_fence_after();
           const float f = ex2_ftz(m_sum - mref);

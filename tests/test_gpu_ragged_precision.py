@@ -1,0 +1,145 @@
+"""GPU tests of how many bits kvq_ragged_attn keeps, on caches whose scores and values
+are chosen so that little else than one rounding shows. Each tolerance is a sum of
+bounds on what is left.
+
+u = 2^-24 is half a step of FP32. The tensor cores round their sums down: less than 2u
+of the running sum for each 16 products added to it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from int8_quantized_paged_quantize_b200 import kvq
+from oracle import formats as OF
+from oracle import paged as OP
+from tests import step_cases as SC
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def given(fmt, ctx, K, V, Hk, G, D):
+    """A filled cache that holds these rows."""
+    f = SC.Filled(fmt, ctx, Hk=Hk, G=G, D=D)
+    f.K, f.V = OF.bf16_round(K.astype(np.float32)), OF.bf16_round(V.astype(np.float32))
+    if f.static:
+        f.static = {s: OF.int8_static_calibrate(x, fmt == "int8c") for s, x in (("k_static", f.K), ("v_static", f.V))}
+    f.pool = OP.LogicalPool(fmt, f.nb, Hk, 16, D, **f.static)
+    f.pool.append(f.K, f.V, f.slots)
+    f.cache = kvq.LayerCache.allocate(fmt, f.dims, **{s: SC.bf16(x).cuda() for s, x in f.static.items()})
+    f.poison()
+    f.cache.append(SC.bf16(f.K).cuda(), SC.bf16(f.V).cuda(), torch.from_numpy(f.slots).cuda())
+    return f
+
+
+def shared(f, q, n, B, f32, sm, window=0):
+    """B sequences of n new tokens each that share the cache's one sequence, and all have
+    the query q [n][Hq][D]: so many that a CTA's share holds whole blocks."""
+    L = f.ctx[0]
+    out = f.cache.ragged(SC.bf16(np.tile(q, (B, 1, 1))).cuda(), SC.i32(np.arange(B + 1) * n), f.d_tables.expand(B, -1).contiguous(),
+                         SC.i32([L] * B), L, sm_scale=sm, window=window, out_dtype=torch.float32 if f32 else torch.bfloat16)
+    assert kvq.device_error() == 0
+    return out.double().cpu().numpy().reshape(B, n, *q.shape[1:])
+
+
+def exact(f, q, sm, window=0):
+    """64-bit attention of the rows q [n][Hq][D], the cache's last n tokens."""
+    (K, V), n, L = f.kv()[0], q.shape[0], f.ctx[0]
+    out = np.empty(q.shape)
+    for i in range(n):
+        end = L - n + i + 1
+        lo = max(0, end - window) if window else 0
+        for h in range(q.shape[1]):
+            s = (K[lo:end, h // f.G] @ q[i, h].astype(np.float64)) * sm
+            w = np.exp(s - s.max())
+            out[i, h] = (w / w.sum()) @ V[lo:end, h // f.G]
+    return out
+
+
+def row_error(out, ref):
+    return float((np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)).max())
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("nats", [12, 20])
+@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2", "bf16", "int8c"])
+def test_small_weights_beside_a_dominant_one(fmt, nats, n):
+    """One token takes nearly all of the softmax and has next to no value; thousands of
+    others, `nats` below it, make up the output. Their weights keep their bits.
+
+    FP32 output, relative to a row: the dominant score, of at most 22 nats, is rounded
+    three times (scale, product, reference): 66u; the others' (at most 3 nats of
+    products, 4 sums of 16 each rounded down): 24u; two exponentials 2^-22 each: 8u; the
+    sums of O: 6 steps of 64 tokens are at most 72 additions, to a sum half as large on
+    average: 72u; with static scales the query's two f16 parts, 2^-22 of 22 nats: 88u.
+    Together below 258u, held to 256u."""
+    L, Hk, G, D, B = 8192, 8, 2, 64, 40
+    rng = np.random.default_rng(1)
+    u = np.where(rng.standard_normal(D) < 0, -1.0, 1.0)
+    static = 5.0 if fmt == "int8c" else 1.0          # a channel's scale is every token's: a longer query, shorter keys
+    K, V = rng.standard_normal((L, Hk, D)) * 0.2 / static, rng.standard_normal((L, Hk, D))
+    K[5], V[5] = (nats + 0.8) / 8 / static * u, 0.0
+    f = given(fmt, [L], K, V, Hk, G, D)
+    q = np.tile(u * static, (n, Hk * G, 1)).astype(np.float32)
+    # single tokens: with a window, which keeps all but the first token, too, as a step
+    # without one may go through the decode kernels
+    for f32, window in ((True, 0), (True, L - 1)):
+        ref = exact(f, q, D ** -0.5, window)
+        out = shared(f, q, n, B, f32, D ** -0.5, window)
+        e = max(row_error(o, ref) for o in out)
+        assert e <= 256 * U, (window, e)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 200])
+@pytest.mark.parametrize("fmt", SC.ALL)
+def test_weights_of_fp32_output(fmt, rows):
+    """Token 0 alone has a value and a weight w in (1/2, 1]; tokens 1 and 2 have the weight
+    1, the others none at all: a row gives w / (w + 2), (w + 1 where it sees no token 2).
+
+    The score is one product, of less than a unit; it is rounded three times (3u), the
+    exponential is 4u off, the weight times the token's scale u, and w moves the result by
+    less than itself: 8u (static scales: the query's two f16 parts, 4u more). The sum of
+    weights, its reciprocal, and the product with it: 4u. Up to three additions rounded
+    down: 6u. Below 24u; a weight of 17 bits is up to 64u off."""
+    Hk, G, D = 2, 8, 64
+    rng = np.random.default_rng(rows)
+    K, V = np.zeros((rows, Hk, D)), np.zeros((rows, Hk, D))
+    K[0, :, 0] = 1.0
+    K[3:, :, 1] = -1.0
+    V[0] = 1.0
+    f = given(fmt, [rows], K, V, Hk, G, D)
+    q = np.zeros((rows, Hk * G, D), np.float32)
+    q[:, :, 0] = -rng.uniform(0.02, 0.98, (rows, Hk * G)) * np.log(2)
+    q[:, :, 1] = 2000.0
+    q = OF.bf16_round(q)
+    ref = exact(f, q, 1.0)
+    n, B = rows, 8
+    out = shared(f, q, n, B, True, 1.0)
+    e = np.abs(out - ref) / np.abs(ref)
+    assert e.max() <= 24 * U, e.max() / U
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+@pytest.mark.parametrize("fmt", SC.ALL)
+def test_sums_of_fp32_output(fmt, n):
+    """8,192 tokens of nearly the same weight and of positive values are added up.
+
+    O is kept by the tensor cores for at most 6 steps of 64 tokens, 12 additions each,
+    rounded down by less than 2u of a sum half as large on average: 72u. Those sums are
+    added in FP32: 8192 / 768 roundings of u, half as large on average: 6u. The scores, of
+    up to 0.7 nats of products (4 sums of 16, rounded down) and three roundings: 8u. The
+    exponential, the sum of weights, the two slots, the division: 14u. Together 100u; the
+    64 steps of a slot, by the tensor cores alone, lose ten times as much as 6 steps do
+    (measured: 19u for 6)."""
+    L, Hk, G, D, B = 8192, 8, 1, 64, 40
+    rng = np.random.default_rng(n)
+    K, V = rng.standard_normal((L, Hk, D)), np.abs(rng.standard_normal((L, Hk, D))) + 0.5
+    f = given(fmt, [L], K, V, Hk, G, D)
+    q = OF.bf16_round((rng.standard_normal((n, Hk * G, D)) * 0.1).astype(np.float32))
+    window = L - 1 if n == 1 else 0                  # no decode step
+    ref = exact(f, q, D ** -0.5, window)
+    out = shared(f, q, n, B, True, D ** -0.5, window)
+    e = np.abs(out - ref) / ref
+    assert e.max() <= 100 * U, e.max() / U
