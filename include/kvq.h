@@ -519,7 +519,7 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
  *
  * Roundings. Sums, maxima and the softmax's sum are FP32. BF16 output: the
  * values code * scale and the softmax weights enter the products rounded to 11
- * bits (BF16 cache: values as stored, weights 8 bits); a token's V keeps them
+ * bits (BF16 cache: values as stored, weights 16 bits); a token's V keeps them
  * while its scale is above 2^-21 of the largest scale of the 64 tokens around it
  * (E5M2: 2^-14). FP32 output: the codes and scales are exact, the weights have 24
  * bits, however far below the largest one they lie. With BF16 output, or a BF16
