@@ -10,28 +10,23 @@
 // steps of 64:
 //   S[128 x 64] = Q . K^T      Q in shared memory, K codes expanded to f16
 //   P = 2^(S f - m)            FP32 registers, one row a thread
-//   O[128 x D] += P . V        P as f16 in tensor memory, V codes as f16
-// The 8-bit codes (INT8: less the zero point) are exact in f16, the query is
-// exact in f16 after a power-of-two scaling of its row (the elements below
-// 2^-29 of the largest aside), and the products accumulate in FP32. A BF16 cache
-// is multiplied as it is stored. Running maximum, sum and O are FP32.
-// The scales of the tokens, two ways:
-//   BF16 output: K and V are expanded to code * scale 2^-e (e of the step and of
-//     K or V: 2^e the power of two above the largest scale, less the room that the
-//     codes leave in f16), rounded to 11 bits;
-//     f = 2^eK sm_scale, and P takes 2^eV. P is rounded to 11 bits (BF16 cache:
-//     17, as two bf16 parts: with one, of 8 bits, 40% of the values came out rounded
-//     otherwise; 1,024 new tokens at 4,096, 64/8 heads, 145 us then, 183 now). The output
-//     itself is rounded to 8. The softmax warps see no scale of a
-//     token: its 64 factors a step and thread, from shared memory, cost them as
-//     much as half of the exponentials.
-//   FP32 output (HP): the codes of K stay as they are, and the scores take the
-//     token's K scale in FP32 and so are those of the dequantized cache. The codes
-//     of V, less their zero point, are exact in bf16, and P takes the token's V scale
-//     in FP32 and is kept to 24 bits as three bf16 parts. bf16 has the range of FP32, so
-//     a weight keeps its bits however far below the largest one it lies: as two f16
-//     parts, thousands of tokens 12 nats below a token without a value came out
-//     4e-3 off (1e-6 now), and 20 nats below it they were lost.
+//   O[128 x D] += P . V        P as bf16 parts in tensor memory, V codes as bf16
+// The query is exact in f16 after a power-of-two scaling of its row (the elements
+// below 2^-29 of the largest aside), the 8-bit codes of K (INT8: less the zero point)
+// are exact in f16 and those of V in bf16, and the products accumulate in FP32. A BF16
+// cache is multiplied as it is stored. Running maximum, sum and O are FP32.
+// The scales of the tokens are applied in FP32: K's to the scores, V's to the weights.
+// A weight is rounded to 16 bits, as two bf16 parts, for BF16 output, which is itself
+// rounded to 8, and to 24, as three, for FP32 output (HP). bf16 has the range of FP32, so a
+// weight keeps its bits however far below the largest one it lies. What was less:
+//   f16 weights (two parts for FP32 output) end at 2^-24: thousands of tokens 12 nats
+//     below a token without a value came out 6e-3 (FP32 output 4e-3) off, and 20 nats
+//     below it they were lost;
+//   K and V expanded to f16 code * scale, with weights of 11 bits, spare the softmax
+//     warps two factors a score from shared memory (1,024 new tokens at 4,096, 64/8 heads:
+//     INT8 202 us, 237 now; FP8 170, 218 now), but 13% of the values came out rounded
+//     otherwise than the exact ones (now 0.2%);
+//   one bf16 part over a BF16 cache: 145 us, 183 now, 40% of the values.
 // With static INT8 scales the K scale of each channel multiplies the query (HP:
 // kept as two f16 parts) and the V scale the finished channel.
 //
@@ -48,7 +43,7 @@
 //
 // The online softmax moves a row's reference m only when the largest weight a
 // step could give, the largest score times 2^eV, passes 2^8 relative to it (O is
-// then rescaled in tensor memory). That also keeps P inside the range of f16.
+// then rescaled in tensor memory).
 //
 // Work split: see kvq_ragged_plan.h. A block that lies in one CTA's share is
 // finished there; the first and the last of a share may be pieces, whose
@@ -61,8 +56,8 @@
 //   2       walks the CTA's share of the work list, hands the pieces to the other
 //           roles through a ring and writes the rows that attend nothing; 3: none
 //   4..7    softmax of slot A (thread = row = TMEM lane), 8..11 of slot B
-//   12..15  converters: codes of a step to f16 (BF16 cache: none), V of tokens
-//           past the end zeroed, the scales as FP32 column factors
+//   12..15  converters: codes of a step to f16 (K) and bf16 (V; BF16 cache: none), V of
+//           tokens past the end zeroed, the scales as FP32 column factors
 // The registers are shared out by role: 168 a thread for the softmax warps
 // (64 scores and the weights made of them), 88 for the others.
 //
@@ -100,8 +95,7 @@ struct RgCfg {
   static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
   // weight parts. The third one has the columns of the slot's S, which its softmax warps have
   // read by then; a slot's next scores are issued behind its values.
-  static constexpr int PP = HP ? 3 : BF ? 2 : 1;
-  static constexpr bool VB = BF || HP;                           // V operand and weights in bf16 (else f16)
+  static constexpr int PP = HP ? 3 : 2;
   // FP32 output: steps of a slot that the tensor cores add up, before its O is added to FP32
   // sums in the workspace (a narrow block's warps have weights for 16 of a step's tokens each,
   // a quarter of the additions). FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392
@@ -110,15 +104,11 @@ struct RgCfg {
   static constexpr int FLUSH = BF ? 4 : 6;
   static __device__ __forceinline__ int flush(int rows) { return rows <= kRgNarrow ? 4 * FLUSH : FLUSH; }
   static constexpr int RPB = QP == 2 ? 128 : 256;     // rows per block
-  // The largest scale of a step is expanded to up to 2^UP, which its codes (448, 255 less
-  // the zero point, 57344) leave room for below 65504. BF16 output: a token keeps its 11
-  // bits while its scale is above 2^-(14 + UP) of the step's largest
-  static constexpr int UP = FMT == KVQ_FP8_E4M3 ? 7 : ZP ? 8 : 0;
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
   static constexpr int NC = BF ? NRAW : 3;                       // operand stages
   static constexpr int CPAGE = kBlockSize * D * 2;               // page at 16 bits
-  static constexpr bool COLS = HP && MV > 0;                     // scores scaled token by token
-  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K and V scale per token; eV, 2^-eV, 2^eK of the step
+  static constexpr bool COLS = MV > 0;                           // scores and weights scaled token by token
+  static constexpr int CMETA = (COLS ? 2 * ST * 4 : 0) + 16;     // K and V scale per token; eV, 2^-eV of the step
   static constexpr int CSTAGE = (BF ? 0 : 2 * PPS * CPAGE) + CMETA;
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr uint32_t K_LBO = 128, K_SBO = 16 * D;
@@ -366,10 +356,6 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0u;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // Four int8 codes less a zero point as f16 (exact): 1024 + (c + 128) by a byte
 // permute, minus z = 1152 + zero point, an integer of [1024, 1279]; z0 for codes
 // 0 and 1, z1 for 2 and 3.
@@ -674,7 +660,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // and a slot's softmax overlaps the other slot's products only.
       if (elect_one()) {
       constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
-      constexpr uint32_t id_pv = idesc_f16(D, C::VB);
+      constexpr uint32_t id_pv = idesc_f16(D, true);
       // operand stages: K pages, then V pages
       const uint32_t q_lo = rg_desc_lo<C::Q_LBO>(smem_u32(qop));
       const uint32_t k_lo = rg_desc_lo<C::K_LBO>(smem_u32(C::BF ? raw : cst));
@@ -891,41 +877,27 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             constexpr int NIT = D / 32;
             const int nv = nvalid(pw);
             uint32_t keep = nv >= 16 ? 0xffffu : (1u << nv) - 1u;   // tokens of the page that count
-            // f16 pairs of neighbouring tokens' V factors and zero points; K factor and
-            // zero point of token `lane % 16`, twice
-            uint32_t vf[C::MV > 0 && !C::VB ? 8 : 1], vz[C::ZP ? 8 : 1];
-            uint32_t kf = 0u, kz = 0u;
+            // f16 pairs of neighbouring tokens' V zero points; K zero point of token
+            // `lane % 16`, twice
+            uint32_t vz[C::ZP ? 8 : 1];
+            uint32_t kz = 0u;
             if constexpr (C::MV > 0) {
-              // the step's largest finite scale: 2^(e + UP) is above it
+              // the step's largest finite V scale
               constexpr int MB = 2 * C::MV;
-              auto top_of = [&](const uint8_t* m) -> uint32_t {
-                uint32_t top = 0u;
+              uint32_t top = 0u;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int t = lane + 32 * z;
-                  uint32_t v = 0u;                           // for a token that holds nothing
-                  if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(m + t * MB);
-                  if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);   // scales are not negative
-                }
-                return __reduce_max_sync(0xffffffffu, top);
-              };
-              // no scale at all (or tiny ones): 2^-100, which leaves the reference to the
-              // steps whose V counts and keeps the sums of 2^(s - m) finite
-              auto exponent = [](uint32_t top) -> int {
-                return top == 0u ? -100 : max(-100, min(126, int(top >> 7) - 126 - C::UP));
-              };
-              int ev, ek = 0;
-              const uint32_t vtop = top_of(mv);
-              if constexpr (HP) {
-                // a step's exponent is taken out of scales beyond 2^60 and 2^-60 only, so
-                // that weights times scales, and their sums, stay within FP32
-                const int e = int(vtop >> 7) - 127;
-                ev = vtop == 0u ? 0 : e > 60 ? e - 60 : e < -60 ? e + 60 : 0;
-              } else {
-                ev = exponent(vtop);
-                ek = exponent(top_of(mk));
+              for (int z = 0; z < 2; ++z) {
+                const int t = lane + 32 * z;
+                uint32_t v = 0u;                             // for a token that holds nothing
+                if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(mv + t * MB);
+                if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);     // scales are not negative
               }
-              const float vdn = __int_as_float((127 - ev) << 23), kdn = __int_as_float((127 - ek) << 23);
+              top = __reduce_max_sync(0xffffffffu, top);
+              // an exponent is taken out of the step's scales when they are beyond 2^60 or
+              // 2^-60 only, so that weights times scales, and their sums, stay within FP32
+              const int e = int(top >> 7) - 127;
+              const int ev = top == 0u ? 0 : e > 60 ? e - 60 : e < -60 ? e + 60 : 0;
+              const float vdn = __int_as_float((127 - ev) << 23);
               // this page's tokens: lane % 16
               const int t = 16 * pw + (lane & 15);
               const bool there = (lane & 15) < nv;
@@ -938,22 +910,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               const uint32_t wm = __ballot_sync(0xffffffffu, wild) & 0xffffu;
               if (wild) sv = plain ? __int_as_float(0x7fc00000) : 0.f;
               if (!plain) keep &= ~wm;
-              // a float of each of the 16 tokens as f16 pairs
-              auto half_bits = [](float x) -> uint32_t { return __half_as_ushort(__float2half_rn(x)); };
-              auto pairs = [&](float x, uint32_t* out) {
-                const uint32_t own = half_bits(x);
-                const uint32_t two = own | (__shfl_xor_sync(0xffffffffu, own, 1) << 16);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) out[j] = __shfl_sync(0xffffffffu, two, 2 * j);
-              };
-              if constexpr (HP) {
-                if (lane < 16) {
-                  cm[t] = sk * qk_scale;
-                  cm[C::ST + t] = sv * vdn;
-                }
-              } else {
-                pairs(sv * vdn, vf);
-                kf = half_bits(sk < INFINITY ? sk * kdn : __int_as_float(0x7fc00000)) * 0x10001u;
+              if (lane < 16) {
+                cm[t] = sk * qk_scale;
+                cm[C::ST + t] = sv * vdn;
               }
               if constexpr (C::ZP) {
                 float zk = 0.f, zv = 0.f;
@@ -961,13 +920,16 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                   zk = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB + 2));
                   zv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB + 2));
                 }
-                pairs(1152.f + zv, vz);
+                auto half_bits = [](float x) -> uint32_t { return __half_as_ushort(__float2half_rn(x)); };
+                const uint32_t own = half_bits(1152.f + zv);
+                const uint32_t two = own | (__shfl_xor_sync(0xffffffffu, own, 1) << 16);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vz[j] = __shfl_sync(0xffffffffu, two, 2 * j);
                 kz = half_bits(1152.f + zk) * 0x10001u;
               }
               if (lane == 0) {
                 if (pw == 0)
-                  *reinterpret_cast<float4*>(cm + (C::COLS ? 2 * C::ST : 0)) =
-                      make_float4(float(ev), vdn, __int_as_float((127 + ek) << 23), 0.f);
+                  *reinterpret_cast<float2*>(cm + 2 * C::ST) = make_float2(float(ev), vdn);
                 const uint32_t bad = plain ? 0u : wm;
                 cmw[4 + pw] = pw < 2 ? bad << (16 * pw) : 0u;
                 cmw[8 + pw] = pw < 2 ? 0u : bad << (16 * (pw - 2));
@@ -984,11 +946,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               uint4 o0, o1;
               if constexpr (C::ZP) codes16_less(codes, __shfl_sync(0xffffffffu, kz, 8 * g + tt), o0, o1);
               else codes16_to_f16<FMT>(codes, o0, o1);
-              if constexpr (C::MV > 0 && !HP) {
-                const uint32_t f = __shfl_sync(0xffffffffu, kf, 8 * g + tt);
-                o0 = make_uint4(mul_f16x2(o0.x, f), mul_f16x2(o0.y, f), mul_f16x2(o0.z, f), mul_f16x2(o0.w, f));
-                o1 = make_uint4(mul_f16x2(o1.x, f), mul_f16x2(o1.y, f), mul_f16x2(o1.z, f), mul_f16x2(o1.w, f));
-              }
               const uint32_t dst = cka + g * 16 * D + (2 * c) * 128 + tt * 16;
               sts_u4(dst, o0.x, o0.y, o0.z, o0.w);
               sts_u4(dst + 128, o1.x, o1.y, o1.z, o1.w);
@@ -1001,13 +958,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               if constexpr (C::ZP) codes16_less_pairs(codes, vz, o0, o1);
               else codes16_to_f16<FMT>(codes, o0, o1);
               uint32_t wv[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-              if constexpr (C::VB) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) wv[j] = f16x2_to_bf16x2(wv[j]);   // exact: codes less zero points
-              } else if constexpr (C::MV > 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) wv[j] = mul_f16x2(wv[j], vf[j]);
-              }
+              for (int j = 0; j < 8; ++j) wv[j] = f16x2_to_bf16x2(wv[j]);   // exact: codes less zero points
               if (!plain) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -1074,7 +1026,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         for (int i = 0; i < NI; ++i) c[rg][i] = have ? src[4 * i] : make_uint4(0, 0, 0, 0);
       }
       uint8_t* dst = qop + (two ? x : 0) * C::QBYTES + quarter * 4 * C::Q_SBO + rs * 16 + cs * C::Q_LBO;
-      // sm_scale is the row factor's, its sign the query's (HP: the tokens' factors have it)
+      // sm_scale is the row factor's, its sign the query's (scales per token: their factors have it)
       if constexpr (C::BF) {
         down = fabsf(qk_scale);
         const uint32_t sg = qk_scale < 0.f ? 0x80008000u : 0u;
@@ -1246,7 +1198,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       if (narrow) {
         const uint32_t z[16] = {};
 #pragma unroll
-        for (int c = 0; c < (C::PP > 1 ? 4 : 2); ++c) tmem_st16(t_p + 16 * c, z);
+        for (int c = 0; c < 4; ++c) tmem_st16(t_p + 16 * c, z);
         tmem_st_wait();
       }
       // operand stage, and its phase, of this slot's first step
@@ -1268,7 +1220,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         tmem_ld_wait();
         tc_fence_before();
         warp_arrive(sfree + x, lane);
-        // HP: the tokens' K and V scales, four at a time; then {eV, 2^-eV, 2^eK}
+        // the tokens' K and V scales, four at a time; then {eV, 2^-eV}
         const float4* cm4 = reinterpret_cast<const float4*>(smem + C::OFF_C + ck * C::CSTAGE + (C::BF ? 0 : 2 * C::PPS * C::CPAGE));
         const int q0 = col0 / 4;
         const uint4 odd = cmask[3 * ck];
@@ -1318,11 +1270,11 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           for (int c = 0; c < NT; ++c)
             if (!(((c < 32 ? v0 : v1) >> (c & 31)) & 1u)) sr[c] = 0xff800000u;
         }
-        float4 ee = make_float4(0.f, 1.f, 1.f, 0.f);       // eV, 2^-eV, 2^eK
-        if constexpr (C::MV > 0) ee = cm4[C::COLS ? C::ST / 2 : 0];
+        float2 ee = make_float2(0.f, 1.f);                 // eV, 2^-eV
+        if constexpr (C::COLS) ee = *reinterpret_cast<const float2*>(cm4 + C::ST / 2);
         // takes x to the base-2 score; never 0 (a score scale of 0, or an underflow), so that
         // masked scores stay -inf
-        const float f = fmaxf(C::COLS ? down : down * ee.z, 1.17549435e-38f);
+        const float f = fmaxf(down, 1.17549435e-38f);
         float mt;
         {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1356,8 +1308,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             tmem_st_wait();
           }
         }
-        // weights 2^(x f - m + eV), as pairs of 16-bit values (HP: times the token's V scale
-        // 2^-eV)
+        // weights 2^(x f - m + eV) times the token's V scale 2^-eV, in parts
         const float mx = ee.x - mref;
         const float2 dn2 = make_float2(f, f), nm2 = make_float2(mx, mx);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1387,19 +1338,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             float2 wv = p2;
             if constexpr (C::COLS)
               wv = __fmul2_rn(p2, (k & 1) ? make_float2(fs[k / 2].z, fs[k / 2].w) : make_float2(fs[k / 2].x, fs[k / 2].y));
-            float2 hv;
-            if constexpr (C::VB) {
-              ph[o] = rg_pack(wv.x, wv.y);
-              if constexpr (C::PP >= 2) hv = make_float2(bf16_lo(ph[o]), bf16_hi(ph[o]));
-            } else {
-              const __half2 f16 = __floats2half2_rn(wv.x, wv.y);
-              ph[o] = *reinterpret_cast<const uint32_t*>(&f16);
-            }
-            if constexpr (C::PP >= 2) {
-              const float2 rest = __ffma2_rn(hv, make_float2(-1.f, -1.f), wv);   // exact
-              pl[o] = rg_pack(rest.x, rest.y);
-              if constexpr (C::PP == 3) pt[o] = rg_pack(rest.x - bf16_lo(pl[o]), rest.y - bf16_hi(pl[o]));
-            }
+            ph[o] = rg_pack(wv.x, wv.y);
+            const float2 rest = __ffma2_rn(make_float2(bf16_lo(ph[o]), bf16_hi(ph[o])), make_float2(-1.f, -1.f), wv);   // exact
+            pl[o] = rg_pack(rest.x, rest.y);
+            if constexpr (C::PP == 3) pt[o] = rg_pack(rest.x - bf16_lo(pl[o]), rest.y - bf16_hi(pl[o]));
           }
           if (c % STC == STC - 1) {
             // the last product has read P
@@ -1409,7 +1351,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
             }
             if constexpr (NCH == 1) {
               tmem_st8(t_p + col0 / 2, ph);
-              if constexpr (C::PP >= 2) tmem_st8(t_p + 32 + col0 / 2, pl);
+              tmem_st8(t_p + 32 + col0 / 2, pl);
               if constexpr (C::PP == 3) {
                 const uint32_t z[8] = {};                  // S was in the other warps' columns
 #pragma unroll
@@ -1423,7 +1365,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               tmem_st8(t_s + 8 * c, pt);
             } else {
               tmem_st16(t_p + 8 * (c - 1), ph);
-              if constexpr (C::PP >= 2) tmem_st16(t_p + 32 + 8 * (c - 1), pl);
+              tmem_st16(t_p + 32 + 8 * (c - 1), pl);
             }
           }
         }

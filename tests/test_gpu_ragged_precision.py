@@ -85,7 +85,7 @@ def test_small_weights_beside_a_dominant_one(fmt, nats, n):
     q = np.tile(u * static, (n, Hk * G, 1)).astype(np.float32)
     # a single token a sequence: with a window, which keeps all but the first token, too,
     # as a step without one may go through the decode kernels (BF16 output: with their roundings)
-    for f32, window in ((True, 0), (True, L - 1)) + (((False, L - 1),) if fmt == "bf16" else ()):
+    for f32, window in ((True, 0), (True, L - 1), (False, L - 1)):
         ref = exact(f, q, D ** -0.5, window)
         out = shared(f, q, n, B, f32, D ** -0.5, window)
         e = max(row_error(o, ref) for o in out)
@@ -145,7 +145,7 @@ def test_sums_of_fp32_output(fmt, n):
     assert e.max() <= 100 * U, e.max() / U
 
 
-@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2", "bf16"])
 @pytest.mark.parametrize("D,window", [(128, 0), (64, 90)])
 def test_bf16_output_is_rounded_once(fmt, D, window):
     """BF16 output is the rounding of what FP32 output holds: all that is rounded on the way
