@@ -518,13 +518,13 @@ int kvq_prefill_attn(const void* q, int32_t batch, int32_t chunk_len, const void
  * id outside the pool (KVQ_DEVERR_BLOCK) is not attended.
  *
  * Roundings. Sums, maxima and the softmax's sum are FP32, the values code * scale
- * exact (static INT8 scales: the query times the K scale has 11 bits for BF16
- * output, 22 for FP32). A softmax weight times its token's V scale is rounded to 16
- * bits for BF16 output and to 24 for FP32 output, however far below the largest one
- * it lies. With BF16 output, or a BF16 cache, sequences with one new token may be
- * served, in calls without a window, by the kernels of kvq_decode_attn, with their
- * roundings: weights of at least 18 bits, with an 8-bit cache above a floor (INT8:
- * 2^-24 of the largest weight times the largest scale of 128 tokens).
+ * exact (static INT8 scales: the query times the K scale has 22 bits). A softmax
+ * weight times its token's V scale is rounded to 16 bits for BF16 output and to 24
+ * for FP32 output, however far below the largest one it lies. With BF16 output, or
+ * a BF16 cache, sequences with one new token may be served, in calls without a
+ * window, by the kernels of kvq_decode_attn, with their roundings: weights of at
+ * least 18 bits, with an 8-bit cache above a floor (INT8: 2^-24 of the largest
+ * weight times the largest scale of 128 tokens).
  *
  * A NaN or an infinity in a V row (with a per-token scale: a scale that is one)
  * makes the rows that attend that token not finite, in its channels or in all of

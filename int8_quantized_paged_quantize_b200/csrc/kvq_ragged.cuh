@@ -27,8 +27,10 @@
 //     INT8 202 us, 237 now; FP8 170, 218 now), but 13% of the values came out rounded
 //     otherwise than the exact ones (now 0.2%);
 //   one bf16 part over a BF16 cache: 145 us, 183 now, 40% of the values.
-// With static INT8 scales the K scale of each channel multiplies the query (HP:
-// kept as two f16 parts) and the V scale the finished channel.
+// With static INT8 scales the K scale of each channel multiplies the query, which is kept
+// as two f16 parts, and the V scale the finished channel. (One part: 4% to 5% of the values
+// at D = 64 rounded otherwise; the second takes the place of slot B's rows, so a block has
+// 128: 1,024 new tokens at 4,096, 64/8 heads, 218 us then, 290 now.)
 //
 // The two halves of the CTA work on different products at the same time, so
 // that one's exponentials cover the other's matrix products: slot A and slot B
@@ -92,7 +94,7 @@ struct RgCfg {
   static constexpr int MV = F8 ? 1 : (ZP ? 2 : 0);
   static constexpr int METAB = kBlockSize * MV * 2;              // raw scale bytes of a page
   static constexpr int ST = kRgStep, PPS = kRgStep / kBlockSize; // tokens, pages per step
-  static constexpr int QP = SI && HP ? 2 : 1;                    // query parts
+  static constexpr int QP = SI ? 2 : 1;                          // query parts
   // weight parts. The third one has the columns of the slot's S, which its softmax warps have
   // read by then; a slot's next scores are issued behind its values.
   static constexpr int PP = HP ? 3 : 2;

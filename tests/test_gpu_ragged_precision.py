@@ -145,7 +145,7 @@ def test_sums_of_fp32_output(fmt, n):
     assert e.max() <= 100 * U, e.max() / U
 
 
-@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2", "bf16"])
+@pytest.mark.parametrize("fmt", SC.ALL)
 @pytest.mark.parametrize("D,window", [(128, 0), (64, 90)])
 def test_bf16_output_is_rounded_once(fmt, D, window):
     """BF16 output is the rounding of what FP32 output holds: all that is rounded on the way
