@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(256, 2) decode_kivi_kernel(
       const int tok0 = tile * 128;
       const int t1 = min(pw.hi * 128, pw.ctx);
       const int npg = min(8, (t1 - tok0 + kBlockSize - 1) / kBlockSize);
-      return p8 < npg ? tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8] : -2;
+      // -2: no page here; any negative id of the table is -1
+      return p8 < npg ? max(tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8], -1) : -2;
     };
     auto step = [&](PieceWalk& pw, int& tile) {
       if (pw.done) return;

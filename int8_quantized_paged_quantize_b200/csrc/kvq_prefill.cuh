@@ -307,12 +307,12 @@ __global__ void __launch_bounds__(448, 1) prefill_mma_kernel(
     const int p8 = lane & 7;
     constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
     const int sp = lane / CPP, sc = lane % CPP;
-    // block id of page p8 of tile `tile` of `pw` (-2: no page there)
+    // block id of page p8 of tile `tile` of `pw` (-2: no page there; a negative id of the table: -1)
     auto load_id = [&](const PieceWalk& pw, int tile) -> int {
       if (lane >= 8 || pw.done) return -2;
       const int tok0 = tile * 128;
       const int npg = min(8, (pw.ctx - tok0 + kBlockSize - 1) / kBlockSize);
-      return p8 < npg ? tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8] : -2;
+      return p8 < npg ? max(tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8], -1) : -2;
     };
     auto step = [&](PieceWalk& pw, int& tile) {
       if (pw.done) return;

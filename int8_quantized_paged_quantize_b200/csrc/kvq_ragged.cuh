@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       int np = 0, i0 = 0;
       bool more = true;
       struct Group {
-        int id, h, n;                          // this lane's block id (-2: no page), head, steps (0: no more)
+        int id, h, n;                          // this lane's block id (-2: no page; a negative one: -1), head, steps (0: no more)
       };
       auto next_item = [&]() {
         more = fetch(np++, it, true);
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         g.h = it.h;
         g.n = min(kRgGroup, it.hi - i0);
         const int pg = (it.first + i0) * C::PPS + lane;
-        if (lane < g.n * C::PPS && int64_t(pg) * kBlockSize < it.ctx) g.id = tables[int64_t(it.b) * bt.W + pg];
+        if (lane < g.n * C::PPS && int64_t(pg) * kBlockSize < it.ctx) g.id = max(tables[int64_t(it.b) * bt.W + pg], -1);
         i0 += g.n;
         if (i0 >= it.hi) next_item();
         return g;
