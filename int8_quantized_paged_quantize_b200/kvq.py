@@ -403,6 +403,14 @@ def _at(dev, t, dtype, name, shape=None):
     return t.data_ptr()
 
 
+def _int32(x, name):
+    """An integer that the C ABI takes in 32 bits (ctypes would cut it)."""
+    v = int(x)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise KvqError(f"{name} must fit 32 bits, not {v}")
+    return v
+
+
 def _cache_at(dev, k_cache, v_cache, k_scale, v_scale):
     """Addresses of the cache arrays, and the pair of scale addresses."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")):
@@ -458,7 +466,8 @@ def _append_rope(dev, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache,
         raise KvqError("cos_sin must be [max_position][rotary_dim]")
     kc, vc, ksc, vsc = _cache_at(dev, k_cache, v_cache, k_scale, v_scale)
     rc = lib().kvq_append_rope(qp, qs, kp, ks, vp, vs, _at(dev, positions, _I32, "positions", (T,)),
-                               _at(dev, cos_sin, _F32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1],
+                               _at(dev, cos_sin, _F32, "cos_sin"), _int32(cos_sin.shape[0], "max_position"),
+                               _int32(cos_sin.shape[1], "rotary_dim"),
                                1 if interleaved else 0, _at(dev, slot_mapping, _I64, "slot_mapping", (T,)),
                                T, qo, kc, vc, ksc, vsc, FMT[fmt], ctypes.byref(d), _raw_stream(dev))
     if rc:
@@ -479,7 +488,7 @@ def read(k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens, to
 
 def _read(dev, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_tokens, total_tokens, fmt,
           d, k_out, v_out, out_dtype):
-    B, total = starts.numel(), int(total_tokens)
+    B, total = starts.numel(), _int32(total_tokens, "total_tokens")
     if total < 0:
         raise KvqError("total_tokens must not be negative")
     if k_out is False and v_out is False:
@@ -513,7 +522,7 @@ def _read(dev, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_toke
 def ragged_workspace_bytes(total_q, fmt, d: Dims):
     """Scratch bytes of kvq_ragged_attn for up to total_q new tokens, on the
     current device."""
-    n = lib().kvq_ragged_attn_workspace_bytes(int(total_q), FMT[fmt], ctypes.byref(d))
+    n = lib().kvq_ragged_attn_workspace_bytes(_int32(total_q, "total_q"), FMT[fmt], ctypes.byref(d))
     if n == 0 and total_q > 0:
         raise KvqError("kvq_ragged_attn_workspace_bytes: invalid arguments")
     return n
@@ -552,8 +561,9 @@ def _ragged_attn(dev, q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
     kc, vc, ks, vs = _cache_at(dev, k_cache, v_cache, k_scale, v_scale)
     rc = lib().kvq_ragged_attn(qp, qs, _at(dev, cu_q, _I32, "cu_q", (B + 1,)), B, T, kc, vc, _PAIR(ks, vs),
                                _at(dev, block_tables, _I32, "block_tables", (B, d.max_blocks_per_seq)),
-                               _at(dev, context_lens, _I32, "context_lens", (B,)), int(max_context_len),
-                               min(int(window), 2 ** 31 - 1), sm_scale, op, 0 if dt is _BF16 else 1, workspace.data_ptr(),
+                               _at(dev, context_lens, _I32, "context_lens", (B,)),
+                               _int32(max_context_len, "max_context_len"),
+                               _int32(min(window, 2 ** 31 - 1), "window"), sm_scale, op, 0 if dt is _BF16 else 1, workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), FMT[fmt], ctypes.byref(d),
                                _raw_stream(dev))
     if rc:
