@@ -387,14 +387,16 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
     const uint64_t pol = l2_evict_first_policy();
     const int p8 = lane & 7;
     constexpr int CPP = C::METAB / 16;                    // 16-byte scale chunks per page
-    // block id of page p8 of tile `tile` of the current piece of `pw`
-    auto load_id = [&](const PieceWalk& pw, int tile) -> int {
-      if (lane >= 8 || pw.done) return -2;
+    // block id of page p8 of tile `tile` of the current piece of `pw`,
+    // and whether this lane has such a page (the table may hold any id)
+    auto load_id = [&](const PieceWalk& pw, int tile, bool& page) -> int {
+      page = false;
+      if (lane >= 8 || pw.done) return -1;
       const int tok0 = tile * 128;
       const int t1 = min(pw.hi * 128, pw.ctx);
       const int npg = min(8, (t1 - tok0 + kBlockSize - 1) / kBlockSize);
-      // -2: no page here; any negative id of the table is -1
-      return p8 < npg ? max(tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8], -1) : -2;
+      page = p8 < npg;
+      return page ? tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8] : -1;
     };
     auto step = [&](PieceWalk& pw, int& tile) {
       if (pw.done) return;
@@ -423,7 +425,8 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
     step(c1, i1);
     step(c2, i2);
     step(c2, i2);
-    int id0 = load_id(c0, i0), id1 = load_id(c1, i1);
+    bool pg0, pg1, pg2;
+    int id0 = load_id(c0, i0, pg0), id1 = load_id(c1, i1, pg1);
     uint4 ksc, vsc;
     load_scales(id0, c0.h, ksc, vsc);
     bool kiss[C::NST], viss[C::NST];
@@ -435,10 +438,10 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
       const uint32_t ph = (gt / C::NST) & 1;
       const int h = c0.h;
       const int id = id0;
-      const int id2 = load_id(c2, i2);
+      const int id2 = load_id(c2, i2, pg2);
       uint4 ksc_n, vsc_n;
-      load_scales(c1.done ? -2 : id1, c1.h, ksc_n, vsc_n);   // next tile's scales, in flight
-      if (lane < 8 && id != -2 && (id < 0 || id >= NB)) flag_error(KVQ_DEVERR_BLOCK);
+      load_scales(c1.done ? -1 : id1, c1.h, ksc_n, vsc_n);   // next tile's scales, in flight
+      if (pg0 && (id < 0 || id >= NB)) flag_error(KVQ_DEVERR_BLOCK);
       const bool valid = lane < 8 && id >= 0 && id < NB;
       const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFFu;
       const int blk = __shfl_sync(0xffffffffu, id, p8);
@@ -475,8 +478,8 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(vfull + s);
       // shift the cursors
-      c0 = c1; i0 = i1; id0 = id1; ksc = ksc_n; vsc = vsc_n;
-      c1 = c2; i1 = i2; id1 = id2;
+      c0 = c1; i0 = i1; id0 = id1; pg0 = pg1; ksc = ksc_n; vsc = vsc_n;
+      c1 = c2; i1 = i2; id1 = id2; pg1 = pg2;
       step(c2, i2);
     }
     if (lane == 0 && *abort_flag) {

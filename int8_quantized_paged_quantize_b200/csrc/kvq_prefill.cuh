@@ -307,12 +307,15 @@ __global__ void __launch_bounds__(448, 1) prefill_mma_kernel(
     const int p8 = lane & 7;
     constexpr int CPP = C::METAB > 0 ? C::METAB / 16 : 1;    // 16-byte scale chunks per page
     const int sp = lane / CPP, sc = lane % CPP;
-    // block id of page p8 of tile `tile` of `pw` (-2: no page there; a negative id of the table: -1)
-    auto load_id = [&](const PieceWalk& pw, int tile) -> int {
-      if (lane >= 8 || pw.done) return -2;
+    // block id of page p8 of tile `tile` of `pw`, and whether this lane has such a page
+    // (the table may hold any id)
+    auto load_id = [&](const PieceWalk& pw, int tile, bool& page) -> int {
+      page = false;
+      if (lane >= 8 || pw.done) return -1;
       const int tok0 = tile * 128;
       const int npg = min(8, (pw.ctx - tok0 + kBlockSize - 1) / kBlockSize);
-      return p8 < npg ? max(tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8], -1) : -2;
+      page = p8 < npg;
+      return page ? tables[int64_t(pw.b) * W + tok0 / kBlockSize + p8] : -1;
     };
     auto step = [&](PieceWalk& pw, int& tile) {
       if (pw.done) return;
@@ -324,7 +327,8 @@ __global__ void __launch_bounds__(448, 1) prefill_mma_kernel(
     PieceWalk c0 = walk, c1 = walk;
     int i0 = walk.lo, i1 = walk.lo;
     step(c1, i1);
-    int id0 = load_id(c0, i0);
+    bool pg0, pg1;
+    int id0 = load_id(c0, i0, pg0);
     bool iss[C::NST];
     uint32_t par[C::NST];
 #pragma unroll
@@ -332,9 +336,9 @@ __global__ void __launch_bounds__(448, 1) prefill_mma_kernel(
     for (int gt = 0; !c0.done; ++gt) {
       const int s = gt % C::NST;
       const uint32_t ph = (gt / C::NST) & 1;
-      const int id1 = load_id(c1, i1);                     // next tile's block ids, in flight
+      const int id1 = load_id(c1, i1, pg1);                     // next tile's block ids, in flight
       const int h = c0.h;
-      if (lane < 8 && id0 != -2 && (id0 < 0 || id0 >= NB)) flag_error(KVQ_DEVERR_BLOCK);
+      if (pg0 && (id0 < 0 || id0 >= NB)) flag_error(KVQ_DEVERR_BLOCK);
       const bool valid = lane < 8 && id0 >= 0 && id0 < NB;
       const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFFu;
       const int blk = __shfl_sync(0xffffffffu, id0, p8);
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(448, 1) prefill_mma_kernel(
         rmask[s] = mask;
         mbar_arrive(rfull + s);
       }
-      c0 = c1; i0 = i1; id0 = id1;
+      c0 = c1; i0 = i1; id0 = id1; pg0 = pg1;
       step(c1, i1);
     }
     if (lane == 0 && *abort_flag) {

@@ -566,19 +566,20 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       int np = 0, i0 = 0;
       bool more = true;
       struct Group {
-        int id, h, n;                          // this lane's block id (-2: no page; a negative one: -1), head, steps (0: no more)
+        int id, h, n, np;                      // this lane's block id, head, steps (0: no more), pages
       };
       auto next_item = [&]() {
         more = fetch(np++, it, true);
         i0 = it.lo;
       };
       auto next_group = [&]() -> Group {
-        Group g{-2, 0, 0};
+        Group g{-1, 0, 0, 0};
         if (!more) return g;
         g.h = it.h;
         g.n = min(kRgGroup, it.hi - i0);
-        const int pg = (it.first + i0) * C::PPS + lane;
-        if (lane < g.n * C::PPS && int64_t(pg) * kBlockSize < it.ctx) g.id = max(tables[int64_t(it.b) * bt.W + pg], -1);
+        const int pg = (it.first + i0) * C::PPS;
+        g.np = min(g.n * C::PPS, (it.ctx + kBlockSize - 1) / kBlockSize - pg);
+        if (lane < g.np) g.id = tables[int64_t(it.b) * bt.W + pg + lane];
         i0 += g.n;
         if (i0 >= it.hi) next_item();
         return g;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           const int u = issued;
           const int id0 = __shfl_sync(0xffffffffu, cur.id, j * C::PPS + (lane & 3));
           const bool valid = lane < C::PPS && id0 >= 0 && id0 < NB;
-          if (lane < C::PPS && id0 != -2 && !valid) flag_error(KVQ_DEVERR_BLOCK);
+          if (lane < C::PPS && j * C::PPS + lane < cur.np && !valid) flag_error(KVQ_DEVERR_BLOCK);
           const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFu;
           const int64_t page = int64_t(id0) * bt.Hk + cur.h;
           uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;
