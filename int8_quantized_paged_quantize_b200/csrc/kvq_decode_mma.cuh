@@ -16,7 +16,8 @@
 // virtual head h, 128-token tile) in order of b, then h, then tile, each (b, h) run
 // also costing kPieceCost units for opening and closing its piece. Each of
 // the N CTA groups takes one contiguous, equal share of the total cost (N
-// is cut so that a share holds at least `unit_tiles` units). A share is a few
+// is cut so that a share holds at least `unit_tiles` units; 0: as many as cut the
+// longest sequence of the batch into slots - 1 runs). A share is a few
 // "pieces", a piece being the share's tiles of one (b, h); each piece ends in
 // an online-softmax partial (max, sum, unnormalised output) in a workspace
 // slot, and the piece holding the last tile of (b, h) records how many slots
@@ -311,23 +312,35 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
   // ------------------------------------------------------------ the share
   // T = total work-list cost; each thread sums the run costs of some sequences
   long long* red64 = reinterpret_cast<long long*>(smem + C::OFF_RED);   // [6] + 2
+  int* redi = reinterpret_cast<int*>(red64 + 8);                        // [6]
   long long* miscll = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);
   int* misci = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
   {
     long long tsum = 0;
+    int longest = 0;                                      // tiles of the longest sequence
     for (int bb = threadIdx.x; bb < B; bb += blockDim.x) {
       const int c = ctx_lens[bb];
       if (c < 0 || c > max_ctx || int64_t(c) > int64_t(W) * kBlockSize) {
         if (blockIdx.x == 0) flag_error(KVQ_DEVERR_CONTEXT);
       } else if (c > 0) {
         tsum += (c + 127) / 128 + kPieceCost;
+        longest = max(longest, (c + 127) / 128);
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tsum += __shfl_xor_sync(0xffffffffu, tsum, o);
     if (lane == 0) red64[warp] = tsum;
+    if (unit_tiles == 0) {                                // uniform: shares sized by the batch
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      if (lane == 0) redi[warp] = longest;
+    }
   }
   __syncthreads();
+  if (unit_tiles == 0) {
+#pragma unroll
+    for (int w = 0; w < 6; ++w) unit_tiles = max(unit_tiles, redi[w]);
+    unit_tiles = (unit_tiles + slots - 2) / (slots - 1);
+  }
   long long T = 0;
 #pragma unroll
   for (int w = 0; w < 6; ++w) T += red64[w];

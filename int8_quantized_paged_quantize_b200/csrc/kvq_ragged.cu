@@ -45,11 +45,17 @@ constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
 constexpr int64_t kRtLong = 32768, kRtWork = 1 << 18;
 
 // The decode kernels' plan: at most kRtSlots partials a row (the automatic plan's
-// number), and kRtRows of them over all sequences.
+// number), and kRtRows of them over all sequences. max_ctx is what the caller allows, in a
+// captured graph the model's maximum, so it sizes the slots only: partition 0 lets the
+// kernel size its shares by the longest sequence of the batch. Contexts of 2,000 tokens, FP8,
+// 32/8 heads, max_ctx exact / 131,072: 1 sequence 15 / 15 us, 8 20 / 20, 64 57 / 57 (shares
+// sized by max_ctx: 15 / 164, 19 / 94, 56 / 96).
 int rt_plan(int32_t n, int32_t max_ctx, const kvq_dims& d, DecodePlan* plan) {
   const int32_t tiles = std::max(1, (max_ctx + kTileTokens - 1) / kTileTokens);
   const int32_t splits = std::min(kRtSlots, kRtRows / n) - 1;
-  return make_plan(n, max_ctx, kTileTokens * ((tiles + splits - 1) / splits), &d, plan);
+  const int rc = make_plan(n, max_ctx, kTileTokens * ((tiles + splits - 1) / splits), &d, plan);
+  plan->partition = 0;
+  return rc;
 }
 // Its workspace for up to n sequences (not falling with n).
 size_t rt_bytes(int32_t n, const kvq_dims& d) {
