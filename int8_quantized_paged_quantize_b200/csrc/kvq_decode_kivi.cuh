@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(256, 2) decode_kivi_kernel(
     // ---------------------------------------------------------- producer
     const uint64_t pol = l2_evict_first_policy();
     const int p8 = lane & 7;
+    // block id of page p8 of tile `tile` of the current piece of `pw`,
     // and whether this lane has such a page (the table may hold any id)
     auto load_id = [&](const PieceWalk& pw, int tile, bool& page) -> int {
       page = false;

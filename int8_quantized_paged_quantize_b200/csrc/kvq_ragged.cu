@@ -64,9 +64,8 @@ size_t rt_bytes(int32_t n, const kvq_dims& d) {
          round256(size_t(n) * d.n_q_heads * sizeof(int32_t));
 }
 
-// Workspace pieces: two places per CTA of `rows` rows each; the sums of its two slots (FP32
-// output); for a decode step each
-// sequence's context and output row, its query and the decode kernels' workspace.
+// Workspace pieces: two places per CTA of `rows` rows each; the sums of its two slots; for a
+// decode step each sequence's context and output row, its query and the decode kernels' workspace.
 struct RgSpace {
   int rows;
   size_t o, ml, pieces, sums, seqs, q1, total;

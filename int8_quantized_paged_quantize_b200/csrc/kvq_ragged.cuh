@@ -98,12 +98,13 @@ struct RgCfg {
   // weight parts. The third one has the columns of the slot's S, which its softmax warps have
   // read by then; a slot's next scores are issued behind its values.
   static constexpr int PP = HP ? 3 : 2;
-  // FP32 output: steps of a slot that the tensor cores add up, before its O is added to FP32
-  // sums in the workspace (a narrow block's warps have weights for 16 of a step's tokens each,
+  // Steps of a slot that the tensor cores add up, before its O is added to FP32 sums in the
+  // workspace: they round their sums down, so that what is lost would grow with the context
+  // (0.1% to 0.2% of a value at 524,288 tokens, BF16 output). FP32 output (a narrow block's warps have weights for 16 of a step's tokens each,
   // a quarter of the additions). FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392
   // with 4 (BF16 cache: 289, 307, 330); rows that see 8,192 tokens are off by 1.5e-6, 1.2e-6,
   // 0.8e-6 (BF16 cache: 1.9e-6, 1.5e-6, 1.1e-6)
-  static constexpr int FLUSH = BF ? 4 : 6;
+  static constexpr int FLUSH = !HP ? 128 : BF ? 4 : 6;
   static __device__ __forceinline__ int flush(int rows) { return rows <= kRgNarrow ? 4 * FLUSH : FLUSH; }
   static constexpr int RPB = QP == 2 ? 128 : 256;     // rows per block
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
         // whether the values of step v are the first of their slot's O
         auto first = [&](int v) -> bool {
           const int k = two ? v : v >> 1;
-          return HP ? k % C::flush(w.rows) == 0 : k == 0;
+          return k % C::flush(w.rows) == 0;
         };
         for (int i = 0; ok && i < steps; ++i) {
           ok = wait(cfull + stage, (par_c >> stage) & 1u);
@@ -1189,7 +1190,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       const int lim_min = __reduce_min_sync(0xffffffffu, lim), lo_max = __reduce_max_sync(0xffffffffu, lo_t);
       float m_run = -INFINITY, mref = 0.f, l = 0.f;   // mref: m_run, or 0 where it is -inf
       bool any_step = false;
-      // FP32 output: the tensor cores round their sums down, by up to a last bit for each
+      // The tensor cores round their sums down, by up to a last bit for each
       // product added; so a slot's O goes to the workspace every FLUSH steps (rows side by
       // side, each thread its own) and is added up there in FP32. m_sum: their reference.
       float* sum = sums + (int64_t(blockIdx.x) * 2 + x) * 128 * D + r;
@@ -1401,7 +1402,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           ++cnt;
           continue;
         }
-        if (HP && (two ? i : i >> 1) % C::flush(pw.rows) == 0 && any_step) {
+        if ((two ? i : i >> 1) % C::flush(pw.rows) == 0 && any_step) {
           wait_all(pvdone + x, (cnt - 1) & 1);
           tc_fence_after();
           const float f = ex2_ftz(m_sum - mref);
@@ -1443,14 +1444,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // ---- the piece's end: O of the last step
       if (any_step) wait_all(pvdone + x, (cnt - 1) & 1);
       tc_fence_after();
-      const float f_sum = HP && summed ? ex2_ftz(m_sum - mref) : 0.f;
+      const float f_sum = summed ? ex2_ftz(m_sum - mref) : 0.f;
       auto add_sums = [&](uint32_t (&ov)[16], int c) {
-        if constexpr (HP) {
-          if (summed) {
+        if (summed) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              ov[e] = __float_as_uint(__uint_as_float(ov[e]) + sum[(16 * c + e) * 128] * f_sum);
-          }
+          for (int e = 0; e < 16; ++e)
+            ov[e] = __float_as_uint(__uint_as_float(ov[e]) + sum[(16 * c + e) * 128] * f_sum);
         }
       };
       const bool whole = pw.lo == 0 && pw.hi == pw.count;
