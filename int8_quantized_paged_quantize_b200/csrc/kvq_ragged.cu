@@ -30,17 +30,20 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 // device, so the choice is by the call's shape; the ragged kernel always runs, leaves the
 // single tokens out and hands their rows on.
 //   total_q = n_seqs, a decode step: always (32/8 heads; 64 sequences of 1,024 to 8,192
-//     tokens: FP8 99 against 270 us, INT8 98 / 327, BF16 177 / 216; 8 of up to 256: 16 / 24;
-//     1 of 100: 14 / 20);
+//     tokens: FP8 108 against 304 us, INT8 107 / 359, BF16 194 / 244; 8 of up to 256, FP8:
+//     16 / 25; 1 of 100: 15 / 22);
 //   total_q > n_seqs, single tokens perhaps beside chunks: 8-bit caches from kRtWork
 //     (sequence, KV head, token)s on. FP8, 63 single tokens and a chunk of 512 at up to
-//     8,000 tokens: 171 / 343 us, 15 and 450 at up to 4,096: 87 / 96, 3 and 500 at 12,000: 140
-//     / 198; two empty launches where no sequence has one token: 8 chunks of 200 181 / 171, 4
-//     of 1,000 507 / 497, 16 of 30 79 / 67. BF16: 244 / 267, 83 / 78, 137 / 139: not worth it.
+//     8,000 tokens: 179 / 347 us, 15 and 450 at up to 4,096: 58 / 73, 3 and 500 at 12,000: 198
+//     / 226. Where no sequence has one token, two launches find nothing to do: 8 chunks of 200
+//     200 / 201, 4 of 1,000 596 / 596, 16 of 30 91 / 80; the lengths are on the device, so that
+//     the shape of the last call is that of 15 and 450. BF16: 277 / 277, 63 / 62, 171 / 170:
+//     not worth it.
 // Not with FP32 output over 8-bit caches: their weights have 18 bits (FP8), or 24 below the
-// largest one (INT8: tokens 12 nats below a dominant one came out 2e-3 off), the ragged
-// kernel's 24 of their own. Nor with contexts above kRtLong for each (sequence, KV head), of which the decode kernels' at
-// most 15 splits leave SMs idle (1 of 60,000 tokens, 1 KV head: 56 / 47 us).
+// largest one (INT8: tokens 12 nats below a dominant one came out 1e-2 off), the ragged
+// kernel's 24 of their own (64 of 1,024 to 8,192 tokens, INT8: 393 us). Nor with contexts
+// above kRtLong for each (sequence, KV head), of which the decode kernels' at most 15 splits
+// leave SMs idle (1 of 60,000 tokens, 1 KV head: 56 / 50 us).
 constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
 constexpr int64_t kRtLong = 32768, kRtWork = 1 << 18;
 

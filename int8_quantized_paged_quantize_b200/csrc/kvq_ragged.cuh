@@ -100,11 +100,15 @@ struct RgCfg {
   static constexpr int PP = HP ? 3 : 2;
   // Steps of a slot that the tensor cores add up, before its O is added to FP32 sums in the
   // workspace: they round their sums down, so that what is lost would grow with the context
-  // (0.1% to 0.2% of a value at 524,288 tokens, BF16 output). FP32 output (a narrow block's warps have weights for 16 of a step's tokens each,
-  // a quarter of the additions). FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392
-  // with 4 (BF16 cache: 289, 307, 330); rows that see 8,192 tokens are off by 1.5e-6, 1.2e-6,
-  // 0.8e-6 (BF16 cache: 1.9e-6, 1.5e-6, 1.1e-6)
-  static constexpr int FLUSH = !HP ? 128 : BF ? 4 : 6;
+  // (0.1% to 0.2% of a value at 524,288 tokens).
+  // BF16 output, INT8, 2 x 2,048 rows at 8,192: 1,613 us with 128 steps, 1,653 with 64, 1,721
+  // with 32; of the values 0.22%, 0.11%, 0.05% are rounded otherwise than by the plain form.
+  // FP32 output, FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392 with 4 (BF16
+  // cache: 289, 307, 330); rows that see 8,192 tokens are off by 1.5e-6, 1.2e-6, 0.8e-6 (BF16
+  // cache: 1.9e-6, 1.5e-6, 1.1e-6).
+  // A narrow block's warps have weights for 16 of a step's tokens each, a quarter of the
+  // additions.
+  static constexpr int FLUSH = !HP ? 64 : BF ? 4 : 6;
   static __device__ __forceinline__ int flush(int rows) { return rows <= kRgNarrow ? 4 * FLUSH : FLUSH; }
   static constexpr int RPB = QP == 2 ? 128 : 256;     // rows per block
   static constexpr int NRAW = BF ? 4 : 3;                        // raw stages (steps)
