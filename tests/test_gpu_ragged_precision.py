@@ -202,3 +202,22 @@ def test_long_contexts_lose_nothing_on_the_way(fmt, n):
             ref[i, h] = (w / w.sum()) @ V[:, h]
     for o in out:
         assert abs(np.mean(o / ref - 1)) <= 1536 * U, np.mean(o / ref - 1)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2", "bf16"])
+def test_values_of_any_size(fmt):
+    """Tokens whose values are 2^100 or 2^-100, alone and beside ordinary ones; a row that
+    does not attend the large ones (they come later, or before its window) keeps its bits.
+    BF16 output: half a step and a little; FP32 output: within 2^-17 of a row, more than
+    the 130u that scores of this size and two steps of sums may cost."""
+    n, ctx = 60, 200
+    for small, large in ((1.0, 2.0 ** 100), (2.0 ** -100, 2.0 ** -100), (2.0 ** -60, 1.0), (2.0 ** 100, 2.0 ** 100)):
+        vf = np.full(ctx, small)
+        vf[170] = large
+        f = SC.Filled(fmt, [ctx], Hk=2, G=4, D=64, row_scale=(np.ones(ctx), vf))
+        q = OF.bf16_round(np.random.default_rng(3).standard_normal((n, 8, 64)).astype(np.float32))
+        for window in (0, 20):
+            ref = exact(f, q, 0.125, window)
+            for f32 in (True, False):
+                out = shared(f, q, n, 3, f32, 0.125, window)
+                assert max(row_error(o, ref) for o in out) <= (2.0 ** -17 if f32 else 2.0 ** -8 + 2.0 ** -16), (small, large, window, f32)
