@@ -317,20 +317,21 @@ __global__ void __maxnreg__(FMT == KVQ_BF16 ? 168 : 120) decode_mma_kernel(
   int* misci = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
   {
     long long tsum = 0;
-    int longest = 0;                                      // tiles of the longest sequence
     for (int bb = threadIdx.x; bb < B; bb += blockDim.x) {
       const int c = ctx_lens[bb];
       if (c < 0 || c > max_ctx || int64_t(c) > int64_t(W) * kBlockSize) {
         if (blockIdx.x == 0) flag_error(KVQ_DEVERR_CONTEXT);
       } else if (c > 0) {
         tsum += (c + 127) / 128 + kPieceCost;
-        longest = max(longest, (c + 127) / 128);
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tsum += __shfl_xor_sync(0xffffffffu, tsum, o);
     if (lane == 0) red64[warp] = tsum;
     if (unit_tiles == 0) {                                // uniform: shares sized by the batch
+      int longest = 0;                                    // tiles of the longest sequence
+      for (int bb = threadIdx.x; bb < B; bb += blockDim.x)
+        longest = max(longest, (mma_seq_ctx(ctx_lens, bb, max_ctx, W) + 127) / 128);
       longest = __reduce_max_sync(0xffffffffu, longest);
       if (lane == 0) redi[warp] = longest;
     }
