@@ -104,8 +104,9 @@ struct RgCfg {
   // BF16 output, INT8, 2 x 2,048 rows at 8,192: 1,613 us with 128 steps, 1,653 with 64, 1,721
   // with 32; of the values 0.22%, 0.11%, 0.05% are rounded otherwise than by the plain form.
   // FP32 output, FP8, 1,024 rows at 4,096: 355 us with 8 steps, 367 with 6, 392 with 4 (BF16
-  // cache: 289, 307, 330); rows that see 8,192 tokens are off by 1.5e-6, 1.2e-6, 0.8e-6 (BF16
-  // cache: 1.9e-6, 1.5e-6, 1.1e-6).
+  // cache: 289, 307, 330); rows that see 8,192 tokens are off by 0.9e-6 with 6 (BF16 cache
+  // 0.9e-6 with 4), and with the parts in the other order by 1.5e-6, 1.2e-6, 0.8e-6 with 8, 6, 4
+  // (BF16 cache 1.9e-6, 1.5e-6, 1.1e-6).
   // A narrow block's warps have weights for 16 of a step's tokens each, a quarter of the
   // additions.
   static constexpr int FLUSH = !HP ? 64 : BF ? 4 : 6;
@@ -666,6 +667,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
       // for O, which reads the third from S's columns:
       //   two blocks of rows  O_A(i-1), S_A(i), O_B(i-1), S_B(i)
       // and a slot's softmax overlaps the other slot's products only.
+      // The smallest part comes first: sums are rounded down, by less while they are small.
       if (elect_one()) {
       constexpr uint32_t id_s = idesc_f16(C::ST, C::BF);
       constexpr uint32_t id_pv = idesc_f16(D, true);
@@ -693,11 +695,11 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           const uint32_t kb = k_lo + uint32_t(stage) * STAGE16;
           const uint32_t qa = q_lo + uint32_t(qx) * (C::QBYTES / 16), ds = tmem + C::COL_S + x * 64;
 #pragma unroll
-          for (int qp = 0; qp < C::QP; ++qp)
+          for (int qp = C::QP - 1; qp >= 0; --qp)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               rg_mma_ss<rg_desc_hi<C::Q_SBO>(), rg_desc_hi<C::K_SBO>()>(
-                  ds, qa + qp * (C::QBYTES / 16) + kk * 16, kb + kk * 16, id_s, (qp | kk) ? 1u : 0u);
+                  ds, qa + qp * (C::QBYTES / 16) + kk * 16, kb + kk * 16, id_s, qp < C::QP - 1 || kk ? 1u : 0u);
           mma_commit(sfull + x);
         }
         return true;
@@ -710,11 +712,11 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
           const uint32_t vb = v_lo + uint32_t(stage) * STAGE16;
           const uint32_t od = tmem + C::COL_O + x * D, pa = tmem + C::COL_P + x * 64;
 #pragma unroll
-          for (int j = 0; j < C::PP; ++j)
+          for (int j = C::PP - 1; j >= 0; --j)
 #pragma unroll
             for (int kk = 0; kk < C::PPS; ++kk)
               rg_mma_ts<rg_desc_hi<C::V_SBO>()>(od, (j < 2 ? pa + j * 32 : tmem + C::COL_S + x * 64) + 8 * kk, vb + kk * (C::CPAGE / 16), id_pv,
-                                                (j | kk) ? 1u : uint32_t(!first));
+                                                j < C::PP - 1 || kk ? 1u : uint32_t(!first));
           mma_commit(pvdone + x);
           if (frees) mma_commit(C::BF ? rfree + stage : cfree + stage);   // the step's last product
         }
