@@ -31,7 +31,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 // single tokens out and hands their rows on.
 //   total_q = n_seqs, a decode step: always (32/8 heads; 64 sequences of 1,024 to 8,192
 //     tokens: FP8 108 against 304 us, INT8 107 / 359, BF16 194 / 244; 8 of up to 256, FP8:
-//     16 / 25; 1 of 100: 15 / 22);
+//     16 / 25; 1 of 100: 15 / 22; 257 of 1,500: 146 / 454, 1,024 of 50 to 1,500: 373 / 1,294);
 //   total_q > n_seqs, single tokens perhaps beside chunks: 8-bit caches from kRtWork
 //     (sequence, KV head, token)s on. FP8, 63 single tokens and a chunk of 512 at up to
 //     8,000 tokens: 179 / 347 us, 15 and 450 at up to 4,096: 58 / 73, 3 and 500 at 12,000: 198
@@ -44,7 +44,8 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 // kernel's 24 of their own (64 of 1,024 to 8,192 tokens, INT8: 393 us). Nor with contexts
 // above kRtLong for each (sequence, KV head), of which the decode kernels' at most 15 splits
 // leave SMs idle (1 of 60,000 tokens, 1 KV head: 56 / 50 us).
-constexpr int kRtSeqs = 256, kRtSlots = 16, kRtRows = 2048;
+// At most kRtSeqs sequences: the workspace has kRtRows partials a head, two a sequence then.
+constexpr int kRtSeqs = 1024, kRtSlots = 16, kRtRows = 2048;
 constexpr int64_t kRtLong = 32768, kRtWork = 1 << 18;
 
 // The decode kernels' plan: at most kRtSlots partials a row (the automatic plan's
@@ -83,7 +84,7 @@ RgSpace rg_space(int32_t total_q, const kvq_dims& d) {
   w.pieces = round256(places * sizeof(RgPiece));
   w.sums = round256(places * 128 * d.head_dim * sizeof(float));
   w.total = w.o + w.ml + w.pieces + w.sums;
-  const int32_t n = std::min(total_q, kRtSeqs);
+  const int32_t n = total_q < 256 ? total_q : kRtSeqs;   // from 256 tokens on, the largest size
   w.seqs = round256(size_t(n) * sizeof(int32_t));
   w.q1 = round256(size_t(n) * d.n_q_heads * d.head_dim * 2);
   w.total += 2 * w.seqs + w.q1 + rt_bytes(n, d);
