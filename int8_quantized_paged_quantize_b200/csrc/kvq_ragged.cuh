@@ -899,8 +899,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
               for (int z = 0; z < 2; ++z) {
                 const int t = lane + 32 * z;
                 uint32_t v = 0u;                             // for a token that holds nothing
-                if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(mv + t * MB);
-                if ((v & 0x7fffu) < 0x7f80u) top = max(top, v);     // scales are not negative
+                if (((pm >> (t >> 4)) & 1u) != 0u && tok0 + t < w.ctx) v = *reinterpret_cast<const uint16_t*>(mv + t * MB) & 0x7fffu;
+                if (v < 0x7f80u) top = max(top, v);
               }
               top = __reduce_max_sync(0xffffffffu, top);
               // an exponent is taken out of the step's scales when they are beyond 2^60 or
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_mma_kernel(
                 sk = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mk + t * MB));
                 sv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(mv + t * MB));
               }
-              const bool wild = !(sv < INFINITY);
+              const bool wild = !(fabsf(sv) < INFINITY);
               const uint32_t wm = __ballot_sync(0xffffffffu, wild) & 0xffffu;
               if (wild) sv = plain ? __int_as_float(0x7fc00000) : 0.f;
               if (!plain) keep &= ~wm;

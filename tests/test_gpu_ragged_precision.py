@@ -221,3 +221,27 @@ def test_values_of_any_size(fmt):
             for f32 in (True, False):
                 out = shared(f, q, n, 3, f32, 0.125, window)
                 assert max(row_error(o, ref) for o in out) <= (2.0 ** -17 if f32 else 2.0 ** -8 + 2.0 ** -16), (small, large, window, f32)
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2"])
+def test_scales_below_zero(fmt, f32):
+    """The quantizers write no negative scale, but a cache may be filled by other means:
+    negative V scales turn the output round, and one of minus infinity shows in the rows
+    that attend its token and in no other."""
+    f = SC.Filled(fmt, [150], D=64, G=2, Hk=1)
+    q = SC.bf16(np.random.default_rng(8).standard_normal((150, 2, 64))).cuda()
+    dt = torch.float32 if f32 else torch.bfloat16
+    call = lambda: f.cache.ragged(q, SC.i32([0, 150]), f.d_tables, SC.i32([150]), 150, out_dtype=dt)  # noqa: E731
+    want = call()
+    scale = f.cache.v_scale[..., 0] if fmt == "int8" else f.cache.v_scale
+    scale.neg_()
+    assert torch.equal(call(), -want)
+    scale.neg_()
+    t = 100
+    slot = int(f.slots[t])
+    scale[slot // 16, 0, slot % 16] = -float("inf")
+    out = call()
+    assert (~torch.isfinite(out[t:])).any(-1).all()
+    assert torch.equal(out[:t], want[:t])
+    assert kvq.device_error() == 0
