@@ -245,3 +245,29 @@ def test_scales_below_zero(fmt, f32):
     assert (~torch.isfinite(out[t:])).any(-1).all()
     assert torch.equal(out[:t], want[:t])
     assert kvq.device_error() == 0
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("fmt", ["fp8", "int8", "e5m2", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_keys_that_are_not_finite(fmt, f32, bad):
+    """A K row (with per-token scales: its scale) that is not finite, or so large that
+    scores overflow, changes no row that does not attend its token."""
+    f = SC.Filled(fmt, [150], D=64, G=2, Hk=1)
+    q = SC.bf16(np.random.default_rng(8).standard_normal((150, 2, 64))).cuda()
+    dt = torch.float32 if f32 else torch.bfloat16
+    call = lambda w: f.cache.ragged(q, SC.i32([0, 150]), f.d_tables, SC.i32([150]), 150, out_dtype=dt, window=w)  # noqa: E731
+    want = {w: call(w) for w in (0, 30)}
+    t = 100
+    slot = int(f.slots[t])
+    if fmt == "bf16":
+        f.cache.k[slot // 16, 0, (slot % 16) // 8, :, slot % 8, :] = bad
+    else:
+        scale = f.cache.k_scale[..., 0] if fmt == "int8" else f.cache.k_scale
+        scale[slot // 16, 0, slot % 16] = bad
+    for w in (0, 30):
+        out = call(w)
+        assert torch.equal(out[:t], want[w][:t])
+        if w:
+            assert torch.equal(out[t + w:], want[w][t + w:])
+    assert kvq.device_error() == 0
