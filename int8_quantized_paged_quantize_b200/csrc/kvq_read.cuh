@@ -87,11 +87,12 @@ __device__ __forceinline__ int warp_upper(const int32_t* cu, int n, int r, int l
   return lo;
 }
 
-// 3 CTAs an SM (80 registers; BF16 pages: 2): 32 whole contexts of 4,100 tokens, 8 KV heads,
-// INT8 167 us against 198 at 128 registers and 212 with K and V in CTAs of their own; 4-bit
-// 57 against 66. At 4 the spills cost more.
+// 3 CTAs an SM (80 registers; BF16 pages and static scales, which spill at 3: 2). 32 whole
+// contexts of 4,100 tokens, 8 KV heads, in a graph: INT8 167 us against 198 at 128 registers
+// and 212 with K and V in CTAs of their own; 4-bit 57 against 66; static scales 265 with 2,
+// 286 with 3. At 4 the spills cost more.
 template <int D, int FMT, typename OutT>
-__global__ void __launch_bounds__(256, FMT == KVQ_BF16 ? 2 : 3) read_kernel(
+__global__ void __launch_bounds__(256, FMT == KVQ_BF16 || FMT == KVQ_INT8_CHANNEL ? 2 : 3) read_kernel(
     const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
     const __nv_bfloat16* __restrict__ ks, const __nv_bfloat16* __restrict__ vs,
     const int32_t* __restrict__ tables, const int32_t* __restrict__ starts,
