@@ -26,7 +26,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Single new tokens, in a call without a window, can go through the decode kernels, which
 // multiply the codes as they are stored: the ragged kernel's converters and producer take
-// 1,800 cycles a step of 64 tokens however few rows there are. The lengths are on the
+// some 2,000 cycles a step of 64 tokens however few rows there are. The lengths are on the
 // device, so the choice is by the call's shape; the ragged kernel always runs, leaves the
 // single tokens out and hands their rows on.
 //   total_q = n_seqs, a decode step: always (32/8 heads; 64 sequences of 1,024 to 8,192

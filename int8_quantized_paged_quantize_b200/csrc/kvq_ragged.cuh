@@ -24,13 +24,13 @@
 //     below it they were lost;
 //   K and V expanded to f16 code * scale, with weights of 11 bits, spare the softmax
 //     warps two factors a score from shared memory (1,024 new tokens at 4,096, 64/8 heads:
-//     INT8 202 us, 237 now; FP8 170, 218 now), but 13% of the values came out rounded
+//     INT8 202 us, 245 now; FP8 170, 219 now), but 13% of the values came out rounded
 //     otherwise than the exact ones (now 0.2%);
-//   one bf16 part over a BF16 cache: 145 us, 183 now, 40% of the values.
+//   one bf16 part over a BF16 cache: 145 us, 175 now, 40% of the values.
 // With static INT8 scales the K scale of each channel multiplies the query, which is kept
 // as two f16 parts, and the V scale the finished channel. (One part: 4% to 5% of the values
 // at D = 64 rounded otherwise; the second takes the place of slot B's rows, so a block has
-// 128: 1,024 new tokens at 4,096, 64/8 heads, 218 us then, 290 now.)
+// 128: 1,024 new tokens at 4,096, 64/8 heads, 218 us then, 310 to 330 now.)
 //
 // The two halves of the CTA work on different products at the same time, so
 // that one's exponentials cover the other's matrix products: slot A and slot B
